@@ -75,10 +75,14 @@ typedef enum moe_format {
                                 w = e2m1(q) * e8m0(s). The 32-element scale block of native
                                 MXFP4 experts (metrale helpers_a.rs, the scale-block note of
                                 transpose_for_prefill_impl) */
-  MOE_FMT_FP8_E4M3 = 5       /* OCP E4M3 codes [n, k], one byte per element; one fp32 scale per
+  MOE_FMT_FP8_E4M3 = 5,      /* OCP E4M3 codes [n, k], one byte per element; one fp32 scale per
                                 expert matrix in tensor_scale; w = e4m3(q) * tensor_scale (the
                                 FP8 grouped decode of metrale forward_fp8_grouped_decode.rs;
                                 the pages give no scale layout, read as per matrix) */
+  MOE_FMT_INT8 = 6           /* signed 8-bit codes [n, k], one byte per element; one fp32 scale
+                                per row (output channel) in scales, n floats per expert;
+                                w = q * scale. Taken by moe_matmul_int8 and the host helpers;
+                                moe_decode_forward refuses it */
 } moe_format;
 
 typedef enum moe_routing {
@@ -127,7 +131,8 @@ typedef struct moe_matrix {
   int32_t format;              /* moe_format */
   int32_t reserved;
   const void* packed;          /* expert 0's weights; 16-byte aligned */
-  const void* scales;          /* Q4: fp16 scales; NVFP4: E4M3, MXFP4: E8M0 block scales */
+  const void* scales;          /* Q4: fp16 scales; NVFP4: E4M3, MXFP4: E8M0 block scales;
+                                  INT8: fp32 channel scales */
   const void* biases;          /* Q4: fp16 biases; else NULL */
   const float* tensor_scale;   /* NVFP4 and FP8: E floats, one per expert; else NULL */
   int64_t expert_stride;       /* bytes from one expert's weights to the next (multiple of 16) */
@@ -262,6 +267,141 @@ int moe_decode_forward_no_alloc(const moe_cfg* cfg, int m, const void* x, const 
                                 void* out, void* stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Row operators: an expert layer over any number of rows                                      */
+/* ------------------------------------------------------------------------------------------ */
+
+/* The steps of the layer as calls of their own, for batches and prompts of any length (the calls
+ * above stop at 64 rows), with expert groups in the router and 8-bit integer experts. Together:
+ *
+ *   moe_route_rows          logits -> experts, weights, and the rows grouped by expert
+ *   moe_quantize_rows_int8  hidden states -> int8 codes and one scale per row
+ *   moe_matmul_int8         gate and up products of each pair's row, act = silu(gate) * up
+ *   moe_quantize_rows_int8  act -> codes and scales
+ *   moe_matmul_int8         down product, rows in expert order
+ *   moe_combine_rows        out[row] = sum over slots of weight * product (+ shared expert)
+ *
+ * All are asynchronous on `stream`, synchronise nothing, allocate nothing, keep nothing between
+ * calls and can be captured into a graph. Pointers are device memory of the current device.
+ * 0 rows are allowed: the call then launches nothing (moe_route_rows still writes its offsets).
+ * Row strides (ld_*) count elements. Buffers that a call writes must not overlap its inputs. */
+
+#define MOE_ROUTE_MAX_EXPERTS 512 /* num_experts of the row operators */
+#define MOE_ROUTE_MAX_TOP_K 16    /* top_k of the row operators */
+#define MOE_ROUTE_MAX_GROUPS 32   /* num_groups */
+
+typedef enum moe_group_score {
+  MOE_GROUP_MAX = 0, /* a group scores as its best expert's selection key */
+  MOE_GROUP_TOP2 = 1 /* ... as the sum of its two largest values: the raw logit when
+                        select_on_raw_logits, else score(l) (+ bias) */
+} moe_group_score;
+
+/* Routing options. num_experts, top_k, routing, norm_topk_prob, select_on_raw_logits,
+ * has_expert_bias and routed_scaling_factor mean what they mean in moe_cfg. */
+typedef struct moe_route_cfg {
+  int32_t num_experts;          /* E: 1..MOE_ROUTE_MAX_EXPERTS */
+  int32_t top_k;                /* k: 1..MOE_ROUTE_MAX_TOP_K, at most topk_groups * E/num_groups */
+  int32_t routing;              /* moe_routing */
+  int32_t norm_topk_prob;
+  int32_t select_on_raw_logits; /* 1: not with softmax, not with a bias */
+  int32_t has_expert_bias;      /* 1: not with softmax */
+  float routed_scaling_factor;
+  int32_t num_groups;           /* G: 1 (no groups)..MOE_ROUTE_MAX_GROUPS; divides E. Group g holds
+                                   the experts [g*E/G, (g+1)*E/G) */
+  int32_t topk_groups;          /* 1..G: only experts of the best topk_groups groups are selected */
+  int32_t group_score;          /* moe_group_score */
+  int32_t logits_dtype;         /* MOE_FMT_F32 or MOE_FMT_BF16 */
+} moe_route_cfg;
+
+/* Bytes of device workspace of moe_route_rows for up to `rows` rows (never shrinks with rows). */
+int moe_route_workspace_bytes(const moe_route_cfg* cfg, int64_t rows, size_t* out_bytes);
+
+/* Route `rows` rows of logits [rows, E] and group their pairs by expert.
+ *  score s  = softmax over the row's experts, sigmoid(l) or sqrt(softplus(l))
+ *  key      = s + bias with a bias, else l (the order of s and of l is the same)
+ *  groups   : the topk_groups groups of the highest score, ties to the lower group
+ *  idx      [rows, k] experts in descending key, ties to the lower id
+ *  weights  [rows, k] s, divided by the sum of the row's k scores when norm_topk_prob, times
+ *           routed_scaling_factor
+ * Keys and group scores are compared as in 64-bit arithmetic: 32-bit ones decide only where
+ * their rounding cannot.
+ * An expert whose logit or key is -infinity or NaN is masked: it is never selected and has no
+ * part in softmax; +infinity counts as the largest finite logit. A slot that finds no expert gets
+ * idx -1 and weight 0 (a fully masked row: all its slots). Under norm_topk_prob the weights of
+ * the filled slots sum to routed_scaling_factor.
+ * sorted_pairs, expert_offsets and token_to_perm (all three or none) are those of
+ * moe_decode_read_routing, for pairs p = r*k + s that have an expert; expert_offsets[E] is their
+ * number. token_to_perm of a pair without one is -1, and so are the entries of sorted_pairs from
+ * expert_offsets[E] on.
+ *  logits     [rows, ld_logits] in cfg->logits_dtype, aligned to its element
+ *  expert_bias float32 [E] when cfg->has_expert_bias, else NULL
+ *  workspace  moe_route_workspace_bytes(cfg, rows) bytes, 256-byte aligned; needs no
+ *             initialisation and holds nothing between calls; NULL is allowed without grouping
+ * Calls that share a workspace must be ordered. rows * k may not pass 2^31 - 1. */
+int moe_route_rows(const moe_route_cfg* cfg, int64_t rows, const void* logits, int64_t ld_logits,
+                   const float* expert_bias, int32_t* idx, float* weights, int32_t* sorted_pairs,
+                   int32_t* expert_offsets, int32_t* token_to_perm, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Symmetric 8-bit quantisation of each row of x[rows, k] (float32 or bfloat16, `x_dtype`):
+ *  scale = max(max|x| / 127, 2^-126) in float32 (1 for an all-zero row)
+ *  q     = x / scale rounded to the nearest integer, ties to even, within -127..127
+ * The rounding is that of the exact quotient. A row that holds a NaN or an infinity gets scale
+ * NaN and codes 0, so that what is computed from it is NaN. Any k >= 1 and any strides; rows that
+ * start on 16 bytes (codes: 8) are read and written in whole vectors. */
+int moe_quantize_rows_int8(int64_t rows, int32_t k, int32_t x_dtype, const void* x, int64_t ld_x,
+                           int8_t* codes, int64_t ld_codes, float* scales, void* stream);
+
+/* Shape and options of moe_matmul_int8. */
+typedef struct moe_matmul_cfg {
+  int32_t n;           /* output channels of one matrix, >= 1 */
+  int32_t k;           /* inputs: a multiple of 16, at most 131056 (sums stay within 32 bits) */
+  int32_t num_experts; /* 1..MOE_ROUTE_MAX_EXPERTS */
+  int32_t top_k;       /* pairs per row of x, read with sorted_pairs (1..MOE_ROUTE_MAX_TOP_K) */
+  int32_t activation;  /* moe_activation, read with a second matrix */
+  int32_t out_dtype;   /* MOE_FMT_F32 or MOE_FMT_BF16 (round to nearest even) */
+} moe_matmul_cfg;
+
+/* Bytes of device workspace of moe_matmul_int8 for up to `rows` output rows. */
+int moe_matmul_workspace_bytes(const moe_matmul_cfg* cfg, int64_t rows, size_t* out_bytes);
+
+/* Product of int8 rows with int8 expert matrices, scaled per row and per channel:
+ *  y[i, j]   = x_scales[r] * scales[e, j] * sum_k x[r, k] * w[e, j, k]    (sums in int32, exact)
+ *  out[i, j] = y, or act(y_w) * y_up when `up` is given (SwiGLU or GeGLU)
+ * for output rows i = 0..rows-1.
+ *  expert_offsets NULL: one matrix (num_experts 1) for every row. Else E+1 ascending positions:
+ *                 rows [expert_offsets[e], expert_offsets[e+1]) use expert e; rows of out from
+ *                 expert_offsets[E] on are left as they were
+ *  sorted_pairs   NULL: r = i (x_rows >= rows). Else r = sorted_pairs[i] / top_k (x holds one
+ *                 row per token); pairs outside [0, x_rows * top_k) leave their row as it was
+ *  pair_weights   NULL, or with sorted_pairs: x_scales[r] is multiplied by
+ *                 pair_weights[sorted_pairs[i]] (the weight on the expert's input)
+ *  x              [x_rows, ld_x] int8, 16-byte aligned, ld_x a multiple of 16
+ *  w, up          host structs of MOE_FMT_INT8 matrices [n, k]; `up` may be NULL
+ *  out            [rows, ld_out] in cfg->out_dtype
+ *  workspace      moe_matmul_workspace_bytes(cfg, rows) bytes, 256-byte aligned, initialised once
+ *                 by moe_workspace_init; moe_get_device_status reads its status
+ * Calls that share a workspace must be ordered. A NaN scale gives NaN outputs. */
+int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const int8_t* x, int64_t ld_x,
+                    const float* x_scales, int64_t rows, const int32_t* expert_offsets,
+                    const int32_t* sorted_pairs, const float* pair_weights, const moe_matrix* w,
+                    const moe_matrix* up, void* out, int64_t ld_out, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Weighted blend of the pairs' rows, the last step of the layer:
+ *  out[r] = sum_{s < top_k} weights[r, s] * y[token_to_perm[r*top_k + s]] + gate[r] * shared[r]
+ * summed in float32 in slot order, the shared expert last.
+ *  y              [y_rows, ld_y] in y_dtype (float32 or bfloat16); positions outside
+ *                 [0, y_rows) (a slot without an expert: -1) add nothing
+ *  weights        float32 [rows, top_k], or NULL for 1 (the weight sat on the expert's input)
+ *  shared         [rows, ld_shared] in y_dtype, or NULL; shared_gate float32 [rows] or NULL for 1
+ *  out            [rows, ld_out] in out_dtype (float32 or bfloat16, round to nearest even) */
+int moe_combine_rows(int64_t rows, int32_t n, int32_t top_k, int32_t y_dtype, const void* y,
+                     int64_t ld_y, int64_t y_rows, const int32_t* token_to_perm,
+                     const float* weights, const void* shared, int64_t ld_shared,
+                     const float* shared_gate, int32_t out_dtype, void* out, int64_t ld_out,
+                     void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Pack and quantise helpers (host memory only, synchronous, no GPU needed)                     */
 /* ------------------------------------------------------------------------------------------ */
 
@@ -295,6 +435,10 @@ int moe_quantize_mxfp4(const float* w, int n, int k, uint8_t* packed, uint8_t* s
  * matrix); each element the nearest E4M3 value of w / tensor_scale (ties to even, saturating at
  * 448). Outputs: packed [n, k] (E4M3 codes), *tensor_scale. */
 int moe_quantize_fp8_e4m3(const float* w, int n, int k, uint8_t* packed, float* tensor_scale);
+
+/* INT8 quantisation of one [n, k] matrix (k a multiple of 16), per row, with the scale and
+ * rounding of moe_quantize_rows_int8. Outputs: packed [n, k] (codes), scales [n]. */
+int moe_quantize_int8(const float* w, int n, int k, int8_t* packed, float* scales);
 
 /* Decode one [n, k] matrix of `format` from host storage to float32 (test aid). For MOE_FMT_F32
  * and MOE_FMT_BF16 `packed` holds the plain matrix. */

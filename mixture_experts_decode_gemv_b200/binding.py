@@ -33,17 +33,24 @@ MOE_MAX_ROWS = 64
 MOE_MAX_EXPERTS = 256
 MOE_MAX_TOP_K = 8
 
+MOE_ROUTE_MAX_EXPERTS = 512
+MOE_ROUTE_MAX_TOP_K = 16
+MOE_ROUTE_MAX_GROUPS = 32
+
 (MOE_FMT_F32, MOE_FMT_BF16, MOE_FMT_Q4_AFFINE_G64, MOE_FMT_NVFP4, MOE_FMT_MXFP4,
- MOE_FMT_FP8_E4M3) = 0, 1, 2, 3, 4, 5
+ MOE_FMT_FP8_E4M3, MOE_FMT_INT8) = 0, 1, 2, 3, 4, 5, 6
 MOE_ROUTE_SOFTMAX, MOE_ROUTE_SIGMOID, MOE_ROUTE_SQRTSOFTPLUS = 0, 1, 2
 MOE_ACT_SWIGLU, MOE_ACT_GEGLU = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 MOE_SHARED_NONE, MOE_SHARED_PLAIN, MOE_SHARED_SIGMOID_GATE = 0, 1, 2
 
 FORMAT_CODES = {"f32": MOE_FMT_F32, "bf16": MOE_FMT_BF16, "q4_affine_g64": MOE_FMT_Q4_AFFINE_G64,
-                "nvfp4": MOE_FMT_NVFP4, "mxfp4": MOE_FMT_MXFP4, "fp8_e4m3": MOE_FMT_FP8_E4M3}
+                "nvfp4": MOE_FMT_NVFP4, "mxfp4": MOE_FMT_MXFP4, "fp8_e4m3": MOE_FMT_FP8_E4M3,
+                "int8": MOE_FMT_INT8}
 ROUTING_CODES = {"softmax": MOE_ROUTE_SOFTMAX, "sigmoid": MOE_ROUTE_SIGMOID,
                  "sqrtsoftplus": MOE_ROUTE_SQRTSOFTPLUS}
 ACTIVATION_CODES = {"swiglu": MOE_ACT_SWIGLU, "geglu": MOE_ACT_GEGLU}
+GROUP_SCORE_CODES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
 SHARED_CODES = {"none": MOE_SHARED_NONE, "plain": MOE_SHARED_PLAIN,
                 "sigmoid_gate": MOE_SHARED_SIGMOID_GATE}
 
@@ -54,7 +61,9 @@ EXPORTS = (
     "moe_quantize_nvfp4", "moe_dequantize", "moe_status_string", "moe_last_cuda_error",
     "moe_version", "moe_decode_forward_no_alloc", "moe_decode_launches",
     "moe_debug_barrier_test", "moe_quantize_mxfp4", "moe_quantize_fp8_e4m3",
-    "moe_debug_set_path", "moe_debug_set_split",
+    "moe_debug_set_path", "moe_debug_set_split", "moe_route_workspace_bytes", "moe_route_rows",
+    "moe_quantize_rows_int8", "moe_matmul_workspace_bytes", "moe_matmul_int8",
+    "moe_combine_rows", "moe_quantize_int8",
 )
 
 MOE_NO_ALLOC_SCRATCH_BYTES = 16 << 20
@@ -94,6 +103,23 @@ class moe_expert_table(ctypes.Structure):
     _fields_ = [("gate", moe_matrix), ("up", moe_matrix), ("down", moe_matrix)]
 
 
+class moe_route_cfg(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("routing", ctypes.c_int32),
+        ("norm_topk_prob", ctypes.c_int32), ("select_on_raw_logits", ctypes.c_int32),
+        ("has_expert_bias", ctypes.c_int32), ("routed_scaling_factor", ctypes.c_float),
+        ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+    ]
+
+
+class moe_matmul_cfg(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32), ("activation", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -123,6 +149,15 @@ def _load() -> ctypes.CDLL:
         "moe_debug_barrier_test": [i32, i64],
         "moe_debug_set_path": [i32],
         "moe_debug_set_split": [i32],
+        "moe_route_workspace_bytes": [P(moe_route_cfg), i64, P(sz)],
+        "moe_route_rows": [P(moe_route_cfg), i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "moe_quantize_rows_int8": [i64, i32, i32, vp, i64, vp, i64, vp, vp],
+        "moe_matmul_workspace_bytes": [P(moe_matmul_cfg), i64, P(sz)],
+        "moe_matmul_int8": [P(moe_matmul_cfg), i64, vp, i64, vp, i64, vp, vp, vp, P(moe_matrix),
+                            P(moe_matrix), vp, i64, vp, sz, vp],
+        "moe_combine_rows": [i64, i32, i32, i32, vp, i64, i64, vp, vp, vp, i64, vp, i32, vp, i64,
+                             vp],
+        "moe_quantize_int8": [vp, i32, i32, vp, vp],
         "moe_status_string": [i32],
         "moe_last_cuda_error": [],
         "moe_version": [],
@@ -256,6 +291,66 @@ def moe_get_device_status(workspace, workspace_bytes: int, stream=None) -> int:
     return st.value
 
 
+# ---- row operators -----------------------------------------------------------------------------
+
+def moe_route_workspace_bytes(cfg: moe_route_cfg, rows: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.moe_route_workspace_bytes(ctypes.byref(cfg), rows, ctypes.byref(out)),
+           "moe_route_workspace_bytes")
+    return out.value
+
+
+def moe_route_rows(cfg: moe_route_cfg, rows: int, logits, ld_logits: int, expert_bias, idx, weights,
+                   sorted_pairs=None, expert_offsets=None, token_to_perm=None, workspace=None,
+                   workspace_bytes: int = 0, stream=None) -> None:
+    """Experts and weights of every row of ``logits`` and, when the three grouping arrays are
+    given, the rows' pairs grouped by expert."""
+    rc = lib.moe_route_rows(
+        ctypes.byref(cfg), rows, _ptr(logits), ld_logits, _ptr(expert_bias), _ptr(idx),
+        _ptr(weights), _ptr(sorted_pairs), _ptr(expert_offsets), _ptr(token_to_perm),
+        _ptr(workspace), workspace_bytes, _stream(stream))
+    _check(rc, "moe_route_rows")
+
+
+def moe_quantize_rows_int8(rows: int, k: int, x_dtype: int, x, ld_x: int, codes, ld_codes: int,
+                           scales, stream=None) -> None:
+    """int8 codes and one float32 scale per row of ``x`` (MOE_FMT_F32 or MOE_FMT_BF16)."""
+    rc = lib.moe_quantize_rows_int8(rows, k, x_dtype, _ptr(x), ld_x, _ptr(codes), ld_codes,
+                                    _ptr(scales), _stream(stream))
+    _check(rc, "moe_quantize_rows_int8")
+
+
+def moe_matmul_workspace_bytes(cfg: moe_matmul_cfg, rows: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.moe_matmul_workspace_bytes(ctypes.byref(cfg), rows, ctypes.byref(out)),
+           "moe_matmul_workspace_bytes")
+    return out.value
+
+
+def moe_matmul_int8(cfg: moe_matmul_cfg, x_rows: int, x, ld_x: int, x_scales, rows: int,
+                    expert_offsets, sorted_pairs, pair_weights, w: moe_matrix,
+                    up: Optional[moe_matrix], out, ld_out: int, workspace, workspace_bytes: int,
+                    stream=None) -> None:
+    """Scaled int8 product of rows with one matrix, or with the experts' matrices (and, with
+    ``up``, the activation of the two products)."""
+    rc = lib.moe_matmul_int8(
+        ctypes.byref(cfg), x_rows, _ptr(x), ld_x, _ptr(x_scales), rows, _ptr(expert_offsets),
+        _ptr(sorted_pairs), _ptr(pair_weights), ctypes.byref(w),
+        ctypes.byref(up) if up is not None else None, _ptr(out), ld_out, _ptr(workspace),
+        workspace_bytes, _stream(stream))
+    _check(rc, "moe_matmul_int8")
+
+
+def moe_combine_rows(rows: int, n: int, top_k: int, y_dtype: int, y, ld_y: int, y_rows: int,
+                     token_to_perm, weights, shared, ld_shared: int, shared_gate, out_dtype: int,
+                     out, ld_out: int, stream=None) -> None:
+    """Weighted sum of each row's expert outputs, plus the (gated) shared expert."""
+    rc = lib.moe_combine_rows(rows, n, top_k, y_dtype, _ptr(y), ld_y, y_rows, _ptr(token_to_perm),
+                              _ptr(weights), _ptr(shared), ld_shared, _ptr(shared_gate), out_dtype,
+                              _ptr(out), ld_out, _stream(stream))
+    _check(rc, "moe_combine_rows")
+
+
 # ---- pack / quantise helpers (host) --------------------------------------------------------------
 
 def moe_packed_bytes(fmt: int, n: int, k: int):
@@ -313,6 +408,16 @@ def moe_quantize_fp8_e4m3(w: np.ndarray):
     _check(lib.moe_quantize_fp8_e4m3(w.ctypes.data, n, k, packed.ctypes.data, ts.ctypes.data),
            "moe_quantize_fp8_e4m3")
     return packed, ts
+
+
+def moe_quantize_int8(w: np.ndarray):
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    n, k = w.shape
+    packed = np.empty((n, k), np.int8)
+    scales = np.empty(n, np.float32)
+    _check(lib.moe_quantize_int8(w.ctypes.data, n, k, packed.ctypes.data, scales.ctypes.data),
+           "moe_quantize_int8")
+    return packed, scales
 
 
 def moe_dequantize(fmt: int, packed: np.ndarray, scales, biases, tensor_scale, n: int, k: int):

@@ -6,6 +6,7 @@ The library is rebuilt only when a source or header is newer than it (or with ``
 from __future__ import annotations
 
 import argparse
+from concurrent.futures import ThreadPoolExecutor
 import os
 import shutil
 import subprocess
@@ -17,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoedecode.so")
 
-SOURCES = ["api.cu", "host_formats.cpp", "no_alloc.cu"]
+SOURCES = ["api.cu", "host_formats.cpp", "no_alloc.cu", "route_rows.cu", "quantize_rows.cu",
+           "matmul_int8.cu", "combine_rows.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -42,26 +44,57 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
-def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False,
-          defines=(), out: str = None) -> str:
-    """Compile the library; ``defines`` (e.g. ``("MOE_PHASE_TIMERS",)``) and ``out`` give a
-    separately named variant build."""
-    target = out or LIB
-    if not force and not defines and out is None and up_to_date():
-        return LIB
-    cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC", "-shared",
-           "-cudart", "static", "--expt-relaxed-constexpr", "-I", INCLUDE,
-           *[f"-D{d}" for d in defines],
-           "-o", target + ".tmp", *[os.path.join(CSRC, s) for s in SOURCES]]
-    if ptxas_verbose:
-        cmd[1:1] = ["-Xptxas", "-v"]
+def _object_up_to_date(obj: str, dep: str) -> bool:
+    """Whether ``obj`` is newer than every file its dependency list names."""
+    if not (os.path.exists(obj) and os.path.exists(dep)):
+        return False
+    text = open(dep).read().replace("\\\n", " ")
+    files = text.split(":", 1)[1].split()
+    t = os.path.getmtime(obj)
+    return all(os.path.exists(f) and os.path.getmtime(f) <= t
+               for f in files + [os.path.abspath(__file__)])
+
+
+def _run(cmd, quiet: bool, verbose: bool) -> None:
     if not quiet:
         print(" ".join(cmd), file=sys.stderr)
     res = subprocess.run(cmd, cwd=CSRC, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
-    if ptxas_verbose or (res.stderr.strip() and not quiet):
+    if verbose or (res.stderr.strip() and not quiet):
         print(res.stderr, file=sys.stderr)
+
+
+def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False,
+          defines=(), out: str = None) -> str:
+    """Compile the library; ``defines`` (e.g. ``("MOE_PHASE_TIMERS",)``) and ``out`` give a
+    separately named variant build. Sources compile in parallel, and one whose object is newer
+    than everything it includes is not compiled again."""
+    target = out or LIB
+    if not force and not defines and out is None and up_to_date():
+        return LIB
+    variant = "-".join(defines) or "default"
+    objdir = os.path.join(PKG, "_build", "".join(c if c.isalnum() or c in "-_" else "_"
+                                                 for c in variant))
+    os.makedirs(objdir, exist_ok=True)
+    flags = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
+             "--expt-relaxed-constexpr", "-I", INCLUDE, *[f"-D{d}" for d in defines]]
+    if ptxas_verbose:
+        flags = ["-Xptxas", "-v", *flags]
+
+    def compile_one(src: str) -> str:
+        obj = os.path.join(objdir, src + ".o")
+        dep = obj + ".d"
+        if force or not _object_up_to_date(obj, dep):
+            _run([_nvcc(), *flags, "-MD", "-MF", dep, "-c", os.path.join(CSRC, src), "-o",
+                  obj + ".tmp.o"], quiet, ptxas_verbose)
+            os.replace(obj + ".tmp.o", obj)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+        objects = list(pool.map(compile_one, SOURCES))
+    _run([_nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", target + ".tmp", *objects], quiet,
+         False)
     os.replace(target + ".tmp", target)
     return target
 

@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "experts.cuh"
 #include "fused.cuh"
+#include "host.h"
 #include "router.cuh"
 #include "tc.cuh"
 
@@ -597,6 +598,13 @@ cudaError_t tc_launch(int fmt, int ntg, bool chain, int sms, cudaStream_t st, co
 }
 
 }  // namespace
+
+// The checks and caches above for the library's other translation units.
+namespace moe_host {
+int fail(int cuda_error) { return cuda_fail((cudaError_t)cuda_error); }
+int supported_device() { return check_device(); }
+int sms() { return sm_count(); }
+}  // namespace moe_host
 
 extern "C" int moe_workspace_bytes(const moe_cfg* cfg, int m, size_t* out_bytes) {
   if (!out_bytes) return MOE_ERR_NULL_POINTER;

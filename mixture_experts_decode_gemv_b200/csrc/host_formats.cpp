@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <algorithm>
+#include <limits>
 
 #include "../../include/moe_decode.h"
 
@@ -134,6 +135,9 @@ extern "C" int moe_packed_bytes(int format, int n, int k, size_t* packed, size_t
     case MOE_FMT_FP8_E4M3:
       if (k % 16) return MOE_ERR_BAD_SHAPE;
       *packed = nk; *scales = 0; *biases = 0; return MOE_OK;
+    case MOE_FMT_INT8:
+      if (k % 16) return MOE_ERR_BAD_SHAPE;
+      *packed = nk; *scales = 4 * (size_t)n; *biases = 0; return MOE_OK;
     default: return MOE_ERR_BAD_FORMAT;
   }
 }
@@ -248,6 +252,37 @@ extern "C" int moe_quantize_fp8_e4m3(const float* w, int n, int k, uint8_t* pack
   return MOE_OK;
 }
 
+extern "C" int moe_quantize_int8(const float* w, int n, int k, int8_t* packed, float* scales) {
+  if (!w || !packed || !scales) return MOE_ERR_NULL_POINTER;
+  if (n <= 0 || k <= 0 || k % 16) return MOE_ERR_BAD_SHAPE;
+  for (int r = 0; r < n; ++r) {
+    const float* row = w + (size_t)r * k;
+    int8_t* q = packed + (size_t)r * k;
+    double amax = 0.0;
+    bool finite = true;
+    for (int j = 0; j < k; ++j) {
+      finite = finite && std::isfinite(row[j]);
+      amax = std::max(amax, std::fabs((double)row[j]));
+    }
+    if (!finite) {
+      scales[r] = std::numeric_limits<float>::quiet_NaN();
+      std::memset(q, 0, (size_t)k);
+      continue;
+    }
+    const float sc = amax > 0.0 ? std::max((float)(amax / 127.0), std::numeric_limits<float>::min())
+                                : 1.0f;
+    scales[r] = sc;
+    // The float64 quotient never rounds onto or across a half: x and (n + 1/2) * scale are
+    // multiples of half an ulp of the scale, so a quotient that is not n + 1/2 is at least 2^-25
+    // away from it.
+    for (int j = 0; j < k; ++j) {
+      const double v = std::nearbyint((double)row[j] / (double)sc);
+      q[j] = (int8_t)std::min(127.0, std::max(-127.0, v));
+    }
+  }
+  return MOE_OK;
+}
+
 extern "C" int moe_dequantize(int format, const void* packed, const void* scales,
                               const void* biases, const float* tensor_scale, int n, int k,
                               float* out) {
@@ -313,6 +348,14 @@ extern "C" int moe_dequantize(int format, const void* packed, const void* scales
       const uint8_t* p = (const uint8_t*)packed;
       const double ts = (double)tensor_scale[0];
       for (size_t i = 0; i < nk; ++i) out[i] = (float)(e4m3_to_double(p[i]) * ts);
+      return MOE_OK;
+    }
+    case MOE_FMT_INT8: {
+      if (!scales) return MOE_ERR_NULL_POINTER;
+      if (k % 16) return MOE_ERR_BAD_SHAPE;
+      const int8_t* p = (const int8_t*)packed;
+      const float* s = (const float*)scales;
+      for (size_t i = 0; i < nk; ++i) out[i] = (float)p[i] * s[i / (size_t)k];
       return MOE_OK;
     }
     default:
