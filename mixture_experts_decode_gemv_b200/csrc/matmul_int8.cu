@@ -6,10 +6,14 @@
 // The sums are int32 and exact (|x|, |w| <= 128 and k <= 131056 keep them below 2^31), so neither
 // tiling nor order can change a bit of them; what follows is float32 and one rounding to the output
 // type.
-#include "host.h"
-#include "rows.cuh"
+#include <mutex>
+
+#include <cuda.h>
 
 #include "common.cuh"
+#include "host.h"
+#include "rows.cuh"
+#include "tc05.cuh"
 
 namespace {
 
@@ -29,11 +33,18 @@ struct MatmulArgs {
   const float* ws;
   const float* ups;
   void* out;
+  int* status;
 };
 
-constexpr int kT = 64;        // rows and channels of a tile
-constexpr int kKB = 64;       // bytes of k per step
-constexpr int kMThreads = 256;
+// ---- tiles ---------------------------------------------------------------------------------------
+//
+// The weights are the M operand (128 channels to a block) and the rows the N operand, so a short
+// group of rows costs only as many columns as it has. With a second matrix the 128 rows of a block's
+// M tile are 16 gate channels, the same 16 up channels, the next 16 gate channels, and so on: gate
+// and up of a channel meet in one warp of the epilogue, 16 lanes apart.
+
+constexpr int kStep = 128;                    // bytes of k per stage: one swizzle atom wide
+constexpr long long kWaitLimit = 2000000000LL;  // about a second of SM clock cycles
 
 // Rows [begin, end) of expert e, within the output whatever the offsets hold.
 __device__ __forceinline__ void expert_range(const MatmulArgs& a, int e, long long& begin,
@@ -45,96 +56,386 @@ __device__ __forceinline__ void expert_range(const MatmulArgs& a, int e, long lo
   }
   begin = max(0, a.offsets[e]);
   end = min((long long)a.offsets[e + 1], a.rows);
+  if (end < begin) end = begin;
 }
 
-// Tiles of 64 rows x 64 channels with dp4a: the plain kernel that every other one is checked
-// against.
-template <bool ACT>
-__global__ void __launch_bounds__(kMThreads) matmul_int8_kernel(const __grid_constant__ MatmulArgs a) {
-  __shared__ int s_x[kT][kKB / 4 + 1], s_w[kT][kKB / 4 + 1], s_u[ACT ? kT : 1][kKB / 4 + 1];
-  __shared__ long long s_row[kT];
-  __shared__ float s_scale[kT];
-  // block y -> (expert, tile of its rows)
-  long long t = blockIdx.y, begin = 0, end = 0;
+// Row of x and factor of output row i; false when its pair lies outside x.
+__device__ __forceinline__ bool source_row(const MatmulArgs& a, long long i, int& row, float& scale) {
+  if (!a.pairs) {
+    row = (int)i;
+    scale = a.x_scales[i];
+    return true;
+  }
+  const int p = a.pairs[i];
+  row = p / a.top_k;
+  if (p < 0 || row >= a.x_rows) return false;
+  scale = a.x_scales[row];
+  if (a.pair_weights) scale *= a.pair_weights[p];
+  return true;
+}
+
+__device__ __forceinline__ void store_one(const MatmulArgs& a, size_t at, float y) {
+  if (a.out_f32) ((float*)a.out)[at] = y;
+  else ((__nv_bfloat16*)a.out)[at] = __float2bfloat16_rn(y);
+}
+
+// ---- many rows: pairs of blocks ------------------------------------------------------------------
+
+constexpr int kPairThreads = 192;   // warp 0 loads, warp 1 issues MMAs, warps 2 to 5 write out
+constexpr int kPairStages = 6;
+constexpr int kPairN = 256;         // rows of a tile at most
+constexpr int kPairA = 128 * kStep, kPairB = (kPairN / 2) * kStep, kPairStage = kPairA + kPairB;
+
+struct PairShared {
+  uint64_t full[kPairStages], empty[kPairStages], done[2], free[2];
+  uint32_t tmem;
+  int abort;
+  int tiles[MOE_ROUTE_MAX_EXPERTS + 1];   // row tiles before each expert
+  float2 cols[2][kPairN];                 // factor of a row, and whether it is written
+};
+constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + sizeof(PairShared);
+
+// Whether any of the 128 threads of the epilogue says so (a barrier for them).
+__device__ __forceinline__ bool any_of_128(bool v) {
+  int r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.s32 p, %1, 0;\n"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n"
+      "selp.s32 %0, 1, 0, q; }"
+      : "=r"(r) : "r"((int)v) : "memory");
+  return r;
+}
+
+// Walks a cluster's tiles: t = row tile * channel tiles + channel tile, in order.
+struct TileWalk {
+  long long t;
   int e = 0;
-  for (; e < a.experts; ++e) {
+  __device__ __forceinline__ explicit TileWalk(long long first) : t(first) {}
+  // Expert, first row, rows and channel tile of tile t; false behind the last.
+  __device__ __forceinline__ bool get(const MatmulArgs& a, const PairShared& sh, int ch_tiles,
+                                      long long& i0, int& live, int& ch) {
+    const long long rt = t / ch_tiles;
+    if (rt >= sh.tiles[a.experts]) return false;
+    ch = (int)(t - rt * ch_tiles);
+    while (sh.tiles[e + 1] <= rt) ++e;
+    long long begin, end;
     expert_range(a, e, begin, end);
-    const long long tiles = end > begin ? (end - begin + kT - 1) / kT : 0;
-    if (t < tiles) break;
-    t -= tiles;
+    const int n = sh.tiles[e + 1] - sh.tiles[e], j = (int)(rt - sh.tiles[e]);
+    // the expert's rows in n nearly equal parts, whole multiples of 32
+    const long long part = ((end - begin + n - 1) / n + 31) / 32 * 32;
+    i0 = begin + j * part;
+    live = (int)max(0LL, min(part, end - i0));
+    return true;
   }
-  if (e == a.experts) return;
-  const long long i0 = begin + t * kT;
-  const int live = (int)min((long long)kT, end - i0);
-  for (int j = threadIdx.x; j < kT; j += kMThreads) {
-    long long row = -1;
-    float sc = 0.f;
-    if (j < live) {
-      row = i0 + j;
-      float pw = 1.f;
-      if (a.pairs) {
-        const int p = a.pairs[i0 + j];
-        row = p >= 0 && p / a.top_k < a.x_rows ? p / a.top_k : -1;
-        if (row >= 0 && a.pair_weights) pw = a.pair_weights[p];
-      }
-      if (row >= 0) sc = a.x_scales[row] * pw;
+};
+
+// Two blocks share a tile of 256 channels (128 with gate and up) x up to 256 rows: each loads half of
+// both operands and holds the accumulators of its channels (int32, 256 columns of tensor memory, two
+// buffers, so that one tile is written out while the next is multiplied).
+template <bool ACT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_up) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  PairShared& sh = *(PairShared*)(base + kPairStages * kPairStage);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  constexpr int kChPair = ACT ? 128 : 256, kChBlock = kChPair / 2;
+  const int ch_tiles = (a.n + kChPair - 1) / kChPair;
+  const int k_steps = (a.k + kStep - 1) / kStep;
+
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      bar_init(smem_addr(&sh.full[s]), 1);
+      bar_init(smem_addr(&sh.empty[s]), 1);
     }
-    s_row[j] = row;
-    s_scale[j] = sc;
+    for (int b = 0; b < 2; ++b) {
+      bar_init(smem_addr(&sh.done[b]), 1);
+      bar_init(smem_addr(&sh.free[b]), 8);   // the epilogue warps of both blocks
+    }
+    bar_init_fence();
+    sh.abort = 0;
   }
+  for (int e = tid; e < a.experts; e += kPairThreads) {
+    long long begin, end;
+    expert_range(a, e, begin, end);
+    sh.tiles[e + 1] = (int)((end - begin + kPairN - 1) / kPairN);
+  }
+  if (warp == 1) tmem_alloc<2>(smem_addr(&sh.tmem), 512);
   __syncthreads();
-  const int n0 = blockIdx.x * kT;
-  const int8_t* w = a.w + (size_t)e * a.w_stride;
-  const int8_t* up = ACT ? a.up + (size_t)e * a.up_stride : nullptr;
-  const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-  int acc[4][4] = {}, acu[4][4] = {};
-  for (int k0 = 0; k0 < a.k; k0 += kKB) {
-    for (int j = threadIdx.x; j < kT * (kKB / 4); j += kMThreads) {
-      const int r = j / (kKB / 4), c = j % (kKB / 4);
-      const bool in_k = k0 + 4 * c < a.k;
-      s_x[r][c] = in_k && s_row[r] >= 0 ? *(const int*)(a.x + (size_t)s_row[r] * a.ld_x + k0 + 4 * c) : 0;
-      const size_t at = (size_t)(n0 + r) * a.k + k0 + 4 * c;
-      s_w[r][c] = in_k && n0 + r < a.n ? *(const int*)(w + at) : 0;
-      if (ACT) s_u[r][c] = in_k && n0 + r < a.n ? *(const int*)(up + at) : 0;
+  if (warp == 0) {
+    int carry = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+      int v = e0 + lane < a.experts ? sh.tiles[e0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += u;
+      }
+      if (e0 + lane < a.experts) sh.tiles[e0 + lane + 1] = v + carry;
+      carry += __shfl_sync(kFull, v, 31);
     }
-    __syncthreads();
-#pragma unroll 4
-    for (int c = 0; c < kKB / 4; ++c) {
-      int xv[4];
+    if (lane == 0) sh.tiles[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const long long first = blockIdx.x / 2, stride = gridDim.x / 2;
+  volatile int* abort = &sh.abort;
+  auto give_up = [&]() {
+    *abort = 1;
+    *a.status = MOE_ERR_DEVICE_TIMEOUT;
+  };
+
+  if (warp == 0) {
+    // ---- loads: this block's 128 rows of weights and its half of the rows of x
+    uint32_t step = 0;
+    TileWalk walk(first);
+    long long i0;
+    int live, ch;
+    bool ok = true;
+    for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride) {
+      const int half = (live + 31) / 32 * 16;
+      const long long r0 = i0 + (long long)rank * half;
+      int rows[4];
+      if (a.pairs) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xv[i] = s_x[tr * 4 + i][c];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int wv = s_w[tc + 16 * j][c], uv = ACT ? s_u[tc + 16 * j][c] : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i][j] = __dp4a(xv[i], wv, acc[i][j]);
-          if (ACT) acu[i][j] = __dp4a(xv[i], uv, acu[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          const long long i = r0 + lane * 4 + j;
+          float unused;
+          int row = 0;
+          rows[j] = i < a.rows && source_row(a, i, row, unused) ? row : 0;
+        }
+      }
+      const uint32_t bytes = 2 * (kPairA + half * kStep);
+      const int ch0 = ch * kChPair + (int)rank * kChBlock;
+      for (int kb = 0; kb < k_steps; ++kb, ++step) {
+        const uint32_t s = step % kPairStages, round = step / kPairStages;
+        ok = bar_wait(smem_addr(&sh.empty[s]), (round & 1) ^ 1, kWaitLimit) && !*abort;
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        const uint32_t full = of_rank(smem_addr(&sh.full[s]), 0);
+        const uint32_t sa = smem_addr(base + s * kPairStage), sb = sa + kPairA;
+        if (rank == 0 && lane == 0) bar_expect(smem_addr(&sh.full[s]), bytes);
+        __syncwarp();
+        const int x = kb * kStep;
+        if constexpr (ACT) {
+          if (lane < 8)
+            tma_load_3d<true>(sa + lane * 2048, (lane & 1) ? &map_up : &map_w, full, x, ch0 + (lane >> 1) * 16, walk.e);
+        } else {
+          if (lane == 0) tma_load_3d<true>(sa, &map_w, full, x, ch0, walk.e);
+        }
+        if (a.pairs) {
+          if (lane * 4 < half) tma_gather4<true>(sb + lane * 512, &map_x, full, x, rows);
+        } else {
+          if (lane * 16 < half) tma_load_2d<true>(sb + lane * 2048, &map_x, full, x, (int)(r0 + lane * 16));
         }
       }
     }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = tr * 4 + i;
-    if (s_row[r] < 0) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + tc + 16 * j;
-      if (c >= a.n) continue;
-      float y = (float)acc[i][j] * s_scale[r] *
-                *(const float*)((const char*)a.ws + (size_t)e * a.ws_stride + (size_t)c * 4);
-      if (ACT) {
-        const float u = (float)acu[i][j] * s_scale[r] *
-                        *(const float*)((const char*)a.ups + (size_t)e * a.ups_stride + (size_t)c * 4);
-        y = moe::act_mul(a.act, y, u);
-      }
-      const size_t o = (size_t)(i0 + r) * a.ld_out + c;
-      if (a.out_f32) ((float*)a.out)[o] = y;
-      else ((__nv_bfloat16*)a.out)[o] = __float2bfloat16_rn(y);
+    // every stage has been read before the block may end
+    for (int j = 0; j < kPairStages; ++j) {
+      if (step <= (uint32_t)j) break;
+      const uint32_t last = step - 1 - j;
+      if (!bar_wait(smem_addr(&sh.empty[last % kPairStages]), (last / kPairStages) & 1, kWaitLimit)) ok = false;
     }
+    if (!ok) give_up();
+  } else if (warp == 1) {
+    // ---- MMAs, by one thread of the first block
+    if (rank == 0 && lane == 0) {
+      uint32_t step = 0, tile = 0;
+      TileWalk walk(first);
+      long long i0;
+      int live, ch;
+      bool ok = true;
+      for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+        const uint32_t b = tile & 1;
+        ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, kWaitLimit) && !*abort;
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t desc = i8_desc(256, (live + 31) / 32 * 32);
+        const uint32_t d = tmem + b * kPairN;
+        for (int kb = 0; kb < k_steps; ++kb, ++step) {
+          const uint32_t s = step % kPairStages, round = step / kPairStages;
+          ok = bar_wait(smem_addr(&sh.full[s]), round & 1, kWaitLimit) && !*abort;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = smem_addr(base + s * kPairStage);
+          const uint64_t da = operand_desc(sa), db = operand_desc(sa + kPairA);
+          const int parts = min(kStep, a.k - kb * kStep + 31) / 32;
+          for (int j = 0; j < parts; ++j)
+            mma_i8<2>(d, da + 2 * j, db + 2 * j, desc, kb > 0 || j > 0);
+          mma_commit<2>(smem_addr(&sh.empty[s]));
+        }
+        if (ok) mma_commit<2>(smem_addr(&sh.done[b]));
+      }
+      if (!ok) give_up();
+    }
+  } else {
+    // ---- epilogue: this warp's 32 channels of every row
+    const int quarter = warp & 3;
+    const int et = tid - 64;
+    uint32_t tile = 0;
+    TileWalk walk(first);
+    long long i0;
+    int live, ch;
+    bool ok = true;
+    for (; walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+      const uint32_t b = tile & 1;
+      float2* cols = sh.cols[b];
+      for (int c = et; c < live; c += 128) {
+        int row;
+        float scale = 0.f;
+        const bool real = source_row(a, i0 + c, row, scale);
+        cols[c] = make_float2(scale, real ? 1.f : 0.f);
+      }
+      const int channel = ACT ? ch * kChPair + (int)rank * kChBlock + quarter * 16 + (lane & 15)
+                              : ch * kChPair + (int)rank * kChBlock + quarter * 32 + lane;
+      const bool in = channel < a.n;
+      const float wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)channel * 4) : 0.f;
+      const float wu = ACT && in
+          ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)channel * 4) : 0.f;
+      // the four warps leave together: one that gave up still comes to the next tile's barrier
+      if (any_of_128(!ok)) break;
+      ok = bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, kWaitLimit) && !*abort;
+      ok = __all_sync(kFull, ok);
+      if (ok) {
+        tc_fence_after();
+        const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
+        for (int c0 = 0; c0 < live; c0 += 32) {
+          int v[32];
+          __syncwarp();
+          tmem_load32(d + c0, v);
+          tmem_load_wait();
+          if constexpr (ACT) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const bool upper = lane & 16;
+              const int got = __shfl_xor_sync(kFull, upper ? v[j] : v[j + 1], 16);
+              const int c = c0 + j + (upper ? 1 : 0);
+              if (c < live && in) {
+                const float2 f = cols[c];
+                const float g = (float)(upper ? got : v[j]) * f.x * wg;
+                const float u = (float)(upper ? v[j + 1] : got) * f.x * wu;
+                if (f.y != 0.f) store_one(a, (size_t)(i0 + c) * a.ld_out + channel, moe::act_mul(a.act, g, u));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int c = c0 + j;
+              if (c < live && in) {
+                const float2 f = cols[c];
+                if (f.y != 0.f) store_one(a, (size_t)(i0 + c) * a.ld_out + channel, (float)v[j] * f.x * wg);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(of_rank(smem_addr(&sh.free[b]), 0));
+      }
+    }
+    if (!ok && lane == 0) give_up();
   }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) tmem_free<2>(tmem, 512);
+}
+
+// ---- host ----------------------------------------------------------------------------------------
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (EncodeTiled)p;
+  }();
+  return fn;
+}
+
+// Rows of k bytes, `box` rows of 128 bytes to a load, swizzled by 128 bytes; bytes past k and rows past
+// the last read as zero.
+bool map_rows(CUtensorMap* m, const void* p, int k, long long rows, long long ld, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t boxes[2] = {kStep, (cuuint32_t)box}, ones[2] = {1, 1};
+  return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void*)p, dims, strides, boxes, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_experts(CUtensorMap* m, const void* p, int k, int n, int experts, long long stride, int box) {
+  const cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)n, (cuuint64_t)experts};
+  const cuuint64_t strides[2] = {(cuuint64_t)k, (cuuint64_t)(experts > 1 ? stride : (long long)n * k)};
+  const cuuint32_t boxes[3] = {kStep, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+  return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void*)p, dims, strides, boxes, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters of two of this kernel that the device holds at once (cached per device).
+template <bool ACT>
+int pair_clusters(cudaError_t* err) {
+  static std::mutex mu;
+  static int cache[64] = {};
+  int dev = 0;
+  *err = cudaGetDevice(&dev);
+  if (*err != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 0 || dev >= 64) return 0;
+  if (!cache[dev]) {
+    *err = cudaFuncSetAttribute(matmul_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+    if (*err != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 74);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    *err = cudaOccupancyMaxActiveClusters(&n, matmul_pair_kernel<ACT>, &cfg);
+    if (*err != cudaSuccess) return 0;
+    cache[dev] = n > 0 ? n : 1;
+  }
+  return cache[dev];
+}
+
+template <bool ACT>
+cudaError_t launch_pair(const MatmulArgs& a, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& up,
+                        cudaStream_t st) {
+  cudaError_t e;
+  const int clusters = pair_clusters<ACT>(&e);
+  if (e != cudaSuccess) return e;
+  const int ch = ACT ? 128 : 256;
+  // every expert may end in a tile that is not full
+  const long long tiles = ((a.rows + kPairN - 1) / kPairN + (a.offsets ? min((long long)a.experts, a.rows) : 0)) *
+                          ((a.n + ch - 1) / ch);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, matmul_pair_kernel<ACT>, a, x, w, up);
 }
 
 int check_cfg(const moe_matmul_cfg* c, int64_t rows) {
@@ -213,11 +514,14 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.up = up ? (const int8_t*)up->packed : nullptr;
   a.ups = up ? (const float*)up->scales : nullptr;
   a.out = out;
-  // every expert may end in a tile that is not full
-  const int64_t tiles = (rows + kT - 1) / kT + (expert_offsets ? c.num_experts : 0);
-  const dim3 grid((unsigned)((c.n + kT - 1) / kT), (unsigned)tiles);
-  if (up) matmul_int8_kernel<true><<<grid, kMThreads, 0, (cudaStream_t)stream>>>(a);
-  else matmul_int8_kernel<false><<<grid, kMThreads, 0, (cudaStream_t)stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  a.status = (int*)workspace;
+  if (!encode_tiled()) return fail(cudaErrorNotSupported);
+  CUtensorMap mx, mw, mu;
+  if (!map_rows(&mx, x, c.k, x_rows, ld_x, sorted_pairs ? 1 : 16) ||
+      !map_experts(&mw, a.w, c.k, c.n, c.num_experts, a.w_stride, up ? 16 : 128) ||
+      !map_experts(&mu, up ? a.up : a.w, c.k, c.n, c.num_experts, up ? a.up_stride : a.w_stride, up ? 16 : 128))
+    return fail(cudaErrorInvalidValue);
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = up ? launch_pair<true>(a, mx, mw, mu, st) : launch_pair<false>(a, mx, mw, mu, st);
   return e == cudaSuccess ? MOE_OK : fail(e);
 }
