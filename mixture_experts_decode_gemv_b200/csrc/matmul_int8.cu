@@ -74,14 +74,20 @@ __device__ __forceinline__ bool source_row(const MatmulArgs& a, long long i, int
   return true;
 }
 
-__device__ __forceinline__ void store_one(const MatmulArgs& a, size_t at, float y) {
-  if (a.out_f32) ((float*)a.out)[at] = y;
-  else ((__nv_bfloat16*)a.out)[at] = __float2bfloat16_rn(y);
+__device__ __forceinline__ void store_one(float* p, float y) { *p = y; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float y) { *p = __float2bfloat16_rn(y); }
+
+// The gated activation with one fast exponential and one fast quotient: 2 + 1.2 |g| units of 2^-23
+// from the exponent's argument, and 2 from the quotient.
+__device__ __forceinline__ float gated(int act, float g, float u) {
+  if (act == MOE_ACT_GEGLU) return moe::gelu_tanh_mul(g, u);
+  return __fdividef(g * u, 1.0f + __expf(-g));
 }
 
 // ---- many rows: pairs of blocks ------------------------------------------------------------------
 
-constexpr int kPairThreads = 192;   // warp 0 loads, warp 1 issues MMAs, warps 2 to 5 write out
+constexpr int kPairEpilogue = 256;  // threads that write out: two warps for each 32 channels
+constexpr int kPairThreads = 64 + kPairEpilogue;   // warp 0 loads, warp 1 issues MMAs
 constexpr int kPairStages = 6;
 constexpr int kPairN = 256;         // rows of a tile at most
 constexpr int kPairA = 128 * kStep, kPairB = (kPairN / 2) * kStep, kPairStage = kPairA + kPairB;
@@ -91,43 +97,82 @@ struct PairShared {
   uint32_t tmem;
   int abort;
   int tiles[MOE_ROUTE_MAX_EXPERTS + 1];   // row tiles before each expert
+  int2 span[MOE_ROUTE_MAX_EXPERTS];       // its first row and its rows
   float2 cols[2][kPairN];                 // factor of a row, and whether it is written
 };
 constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + sizeof(PairShared);
 
-// Whether any of the 128 threads of the epilogue says so (a barrier for them).
-__device__ __forceinline__ bool any_of_128(bool v) {
+// Whether any thread of the epilogue says so (a barrier for them).
+__device__ __forceinline__ bool any_writer(bool v) {
   int r;
   asm volatile(
       "{ .reg .pred p, q; setp.ne.s32 p, %1, 0;\n"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n"
       "selp.s32 %0, 1, 0, q; }"
-      : "=r"(r) : "r"((int)v) : "memory");
+      : "=r"(r) : "r"((int)v), "n"(kPairEpilogue) : "memory");
   return r;
 }
 
-// Walks a cluster's tiles: t = row tile * channel tiles + channel tile, in order.
+// Walks a cluster's tiles in order. The tiles of an expert go in bands of kBand row tiles: within a
+// band the row tiles of one channel tile come one after another, so that the clusters at work share
+// kBand row tiles and a few channel tiles, which L2 holds.
+constexpr int kBand = 8;
 struct TileWalk {
-  long long t;
-  int e = 0;
-  __device__ __forceinline__ explicit TileWalk(long long first) : t(first) {}
-  // Expert, first row, rows and channel tile of tile t; false behind the last.
-  __device__ __forceinline__ bool get(const MatmulArgs& a, const PairShared& sh, int ch_tiles,
-                                      long long& i0, int& live, int& ch) {
-    const long long rt = t / ch_tiles;
-    if (rt >= sh.tiles[a.experts]) return false;
-    ch = (int)(t - rt * ch_tiles);
-    while (sh.tiles[e + 1] <= rt) ++e;
-    long long begin, end;
-    expert_range(a, e, begin, end);
-    const int n = sh.tiles[e + 1] - sh.tiles[e], j = (int)(rt - sh.tiles[e]);
+  int t, e = 0;
+  __device__ __forceinline__ explicit TileWalk(int first) : t(first) {}
+  // First row, rows and channel tile of tile t, and its expert in e; false behind the last.
+  __device__ __forceinline__ bool get(const MatmulArgs& a, const PairShared& sh, int ch_tiles, int& i0,
+                                      int& live, int& ch) {
+    if (t >= sh.tiles[a.experts] * ch_tiles) return false;
+    while (sh.tiles[e + 1] * ch_tiles <= t) ++e;
+    const int n = sh.tiles[e + 1] - sh.tiles[e];
+    int r = t - sh.tiles[e] * ch_tiles;
+    const int band = r / (kBand * ch_tiles);
+    r -= band * kBand * ch_tiles;
+    const int wide = min(kBand, n - band * kBand);
+    ch = r / wide;
+    const int j = band * kBand + r - ch * wide;
     // the expert's rows in n nearly equal parts, whole multiples of 32
-    const long long part = ((end - begin + n - 1) / n + 31) / 32 * 32;
-    i0 = begin + j * part;
-    live = (int)max(0LL, min(part, end - i0));
+    const int2 span = sh.span[e];
+    const int part = ((span.y - 1) / n + 32) & ~31;
+    i0 = span.x + j * part;
+    live = min(part, span.y - j * part);
     return true;
   }
 };
+
+// One warp's share of a finished tile: its 32 lanes' channels of every second chunk of 32 rows. `out`
+// points at the thread's channel of the tile's first row, `d` at the warp's lanes in tensor memory.
+template <bool ACT, typename T>
+__device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t d, const float2* cols, int live,
+                                           int first_chunk, bool in, float wg, float wu) {
+  const bool upper = threadIdx.x & 16;
+  const long long ld = a.ld_out;
+  for (int c0 = 32 * first_chunk; c0 < live; c0 += 64) {
+    int v[32];
+    __syncwarp();
+    tmem_load32(d + c0, v);
+    tmem_load_wait();
+    T* p = out + c0 * ld;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float4 f = *(const float4*)(cols + c0 + j);
+      if constexpr (ACT) {
+        // the lower half of the warp holds gate and takes row j, the upper holds up and takes row j + 1
+        const int got = __shfl_xor_sync(kFull, upper ? v[j] : v[j + 1], 16);
+        const float s = upper ? f.z : f.x;
+        const float g = (float)(upper ? got : v[j]) * s * wg;
+        const float u = (float)(upper ? v[j + 1] : got) * s * wu;
+        const float y = gated(a.act, g, u);
+        if (in && (upper ? f.w : f.y) != 0.f) store_one(p + (upper ? ld : 0), y);
+      } else {
+        if (in && f.y != 0.f) store_one(p, (float)v[j] * f.x * wg);
+        if (in && f.w != 0.f) store_one(p + ld, (float)v[j + 1] * f.z * wg);
+      }
+      p += 2 * ld;
+    }
+  }
+}
 
 // Two blocks share a tile of 256 channels (128 with gate and up) x up to 256 rows: each loads half of
 // both operands and holds the accumulators of its channels (int32, 256 columns of tensor memory, two
@@ -152,7 +197,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(smem_addr(&sh.done[b]), 1);
-      bar_init(smem_addr(&sh.free[b]), 8);   // the epilogue warps of both blocks
+      bar_init(smem_addr(&sh.free[b]), 2 * kPairEpilogue / 32);   // the epilogue warps of both blocks
     }
     bar_init_fence();
     sh.abort = 0;
@@ -161,6 +206,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     long long begin, end;
     expert_range(a, e, begin, end);
     sh.tiles[e + 1] = (int)((end - begin + kPairN - 1) / kPairN);
+    sh.span[e] = make_int2((int)begin, (int)(end - begin));
   }
   if (warp == 1) tmem_alloc<2>(smem_addr(&sh.tmem), 512);
   __syncthreads();
@@ -183,45 +229,38 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const long long first = blockIdx.x / 2, stride = gridDim.x / 2;
+  const int first = blockIdx.x / 2, stride = gridDim.x / 2;
   volatile int* abort = &sh.abort;
-  auto give_up = [&]() {
-    *abort = 1;
-    *a.status = MOE_ERR_DEVICE_TIMEOUT;
-  };
+  bool ok = true;
 
   if (warp == 0) {
     // ---- loads: this block's 128 rows of weights and its half of the rows of x
-    uint32_t step = 0;
+    uint32_t s = 0, parity = 1;
     TileWalk walk(first);
-    long long i0;
-    int live, ch;
-    bool ok = true;
+    int i0, live, ch;
     for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride) {
       const int half = (live + 31) / 32 * 16;
-      const long long r0 = i0 + (long long)rank * half;
+      const int r0 = i0 + (int)rank * half;
       int rows[4];
       if (a.pairs) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const long long i = r0 + lane * 4 + j;
+          const int i = r0 + lane * 4 + j;
           float unused;
           int row = 0;
           rows[j] = i < a.rows && source_row(a, i, row, unused) ? row : 0;
         }
       }
-      const uint32_t bytes = 2 * (kPairA + half * kStep);
+      const uint32_t bytes = 2 * (kPairA + (a.pairs ? half : 128) * kStep);
       const int ch0 = ch * kChPair + (int)rank * kChBlock;
-      for (int kb = 0; kb < k_steps; ++kb, ++step) {
-        const uint32_t s = step % kPairStages, round = step / kPairStages;
-        ok = bar_wait(smem_addr(&sh.empty[s]), (round & 1) ^ 1, kWaitLimit) && !*abort;
-        ok = __all_sync(kFull, ok);
+      for (int kb = 0; kb < k_steps; ++kb) {
+        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
         if (!ok) break;
         const uint32_t full = of_rank(smem_addr(&sh.full[s]), 0);
         const uint32_t sa = smem_addr(base + s * kPairStage), sb = sa + kPairA;
+        const int x = kb * kStep;
         if (rank == 0 && lane == 0) bar_expect(smem_addr(&sh.full[s]), bytes);
         __syncwarp();
-        const int x = kb * kStep;
         if constexpr (ACT) {
           if (lane < 8)
             tma_load_3d<true>(sa + lane * 2048, (lane & 1) ? &map_up : &map_w, full, x, ch0 + (lane >> 1) * 16, walk.e);
@@ -231,64 +270,73 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
         if (a.pairs) {
           if (lane * 4 < half) tma_gather4<true>(sb + lane * 512, &map_x, full, x, rows);
         } else {
-          if (lane * 16 < half) tma_load_2d<true>(sb + lane * 2048, &map_x, full, x, (int)(r0 + lane * 16));
+          if (lane == 0) tma_load_2d<true>(sb, &map_x, full, x, r0);
+        }
+        if (++s == kPairStages) {
+          s = 0;
+          parity ^= 1;
         }
       }
     }
     // every stage has been read before the block may end
-    for (int j = 0; j < kPairStages; ++j) {
-      if (step <= (uint32_t)j) break;
-      const uint32_t last = step - 1 - j;
-      if (!bar_wait(smem_addr(&sh.empty[last % kPairStages]), (last / kPairStages) & 1, kWaitLimit)) ok = false;
+    for (int j = 0; ok && j < kPairStages; ++j) {
+      ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+      if (++s == kPairStages) {
+        s = 0;
+        parity ^= 1;
+      }
     }
-    if (!ok) give_up();
   } else if (warp == 1) {
-    // ---- MMAs, by one thread of the first block
-    if (rank == 0 && lane == 0) {
-      uint32_t step = 0, tile = 0;
+    // ---- MMAs, issued by one lane of the first block. The loop stays uniform over the warp and the
+    // four MMAs of a step unrolled: with a run-time count under a divergent branch the issue took
+    // 190 cycles per MMA, more than the 128 that the MMA itself takes. Past k both operands are zero.
+    if (rank == 0) {
+      uint32_t s = 0, parity = 0, tile = 0;
+      const uint64_t desc0 = operand_desc(smem_addr(base));
       TileWalk walk(first);
-      long long i0;
-      int live, ch;
-      bool ok = true;
+      int i0, live, ch;
       for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
         const uint32_t b = tile & 1;
-        ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, kWaitLimit) && !*abort;
+        ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
         if (!ok) break;
         tc_fence_after();
         const uint32_t desc = i8_desc(256, (live + 31) / 32 * 32);
         const uint32_t d = tmem + b * kPairN;
-        for (int kb = 0; kb < k_steps; ++kb, ++step) {
-          const uint32_t s = step % kPairStages, round = step / kPairStages;
-          ok = bar_wait(smem_addr(&sh.full[s]), round & 1, kWaitLimit) && !*abort;
+        for (int kb = 0; kb < k_steps; ++kb) {
+          ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, kWaitLimit);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_addr(base + s * kPairStage);
-          const uint64_t da = operand_desc(sa), db = operand_desc(sa + kPairA);
-          const int parts = min(kStep, a.k - kb * kStep + 31) / 32;
-          for (int j = 0; j < parts; ++j)
-            mma_i8<2>(d, da + 2 * j, db + 2 * j, desc, kb > 0 || j > 0);
-          mma_commit<2>(smem_addr(&sh.empty[s]));
+          if (elect()) {
+            const uint64_t da = desc0 + s * (kPairStage >> 4), db = da + (kPairA >> 4);
+            mma_i8<2>(d, da, db, desc, kb > 0);
+            mma_i8<2>(d, da + 2, db + 2, desc, true);
+            mma_i8<2>(d, da + 4, db + 4, desc, true);
+            mma_i8<2>(d, da + 6, db + 6, desc, true);
+            mma_commit<2>(smem_addr(&sh.empty[s]));
+            if (kb + 1 == k_steps) mma_commit<2>(smem_addr(&sh.done[b]));
+          }
+          __syncwarp();
+          if (++s == kPairStages) {
+            s = 0;
+            parity ^= 1;
+          }
         }
-        if (ok) mma_commit<2>(smem_addr(&sh.done[b]));
       }
-      if (!ok) give_up();
     }
   } else {
-    // ---- epilogue: this warp's 32 channels of every row
-    const int quarter = warp & 3;
+    // ---- epilogue: this warp's 32 channels of every second 32 rows
+    const int quarter = warp & 3, first_chunk = (warp - 2) >> 2;
     const int et = tid - 64;
     uint32_t tile = 0;
     TileWalk walk(first);
-    long long i0;
-    int live, ch;
-    bool ok = true;
+    int i0, live, ch;
     for (; walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
       float2* cols = sh.cols[b];
-      for (int c = et; c < live; c += 128) {
+      for (int c = et; c < (live + 31) / 32 * 32; c += kPairEpilogue) {
         int row;
         float scale = 0.f;
-        const bool real = source_row(a, i0 + c, row, scale);
+        const bool real = c < live && source_row(a, i0 + c, row, scale);
         cols[c] = make_float2(scale, real ? 1.f : 0.f);
       }
       const int channel = ACT ? ch * kChPair + (int)rank * kChBlock + quarter * 16 + (lane & 15)
@@ -297,48 +345,27 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       const float wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)channel * 4) : 0.f;
       const float wu = ACT && in
           ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)channel * 4) : 0.f;
-      // the four warps leave together: one that gave up still comes to the next tile's barrier
-      if (any_of_128(!ok)) break;
-      ok = bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, kWaitLimit) && !*abort;
-      ok = __all_sync(kFull, ok);
+      // the warps leave together: one that gave up still comes to the next tile's barrier
+      if (any_writer(!ok)) {
+        ok = false;
+        break;
+      }
+      ok = bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
       if (ok) {
         tc_fence_after();
         const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
-        for (int c0 = 0; c0 < live; c0 += 32) {
-          int v[32];
-          __syncwarp();
-          tmem_load32(d + c0, v);
-          tmem_load_wait();
-          if constexpr (ACT) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const bool upper = lane & 16;
-              const int got = __shfl_xor_sync(kFull, upper ? v[j] : v[j + 1], 16);
-              const int c = c0 + j + (upper ? 1 : 0);
-              if (c < live && in) {
-                const float2 f = cols[c];
-                const float g = (float)(upper ? got : v[j]) * f.x * wg;
-                const float u = (float)(upper ? v[j + 1] : got) * f.x * wu;
-                if (f.y != 0.f) store_one(a, (size_t)(i0 + c) * a.ld_out + channel, moe::act_mul(a.act, g, u));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int c = c0 + j;
-              if (c < live && in) {
-                const float2 f = cols[c];
-                if (f.y != 0.f) store_one(a, (size_t)(i0 + c) * a.ld_out + channel, (float)v[j] * f.x * wg);
-              }
-            }
-          }
-        }
+        const size_t at = (size_t)i0 * a.ld_out + channel;
+        if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, cols, live, first_chunk, in, wg, wu);
+        else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, cols, live, first_chunk, in, wg, wu);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive_cluster(of_rank(smem_addr(&sh.free[b]), 0));
       }
     }
-    if (!ok && lane == 0) give_up();
+  }
+  if (!ok) {   // a wait ran out: the others are told, and the host finds it in the workspace
+    *abort = 1;
+    *a.status = MOE_ERR_DEVICE_TIMEOUT;
   }
   __syncwarp();
   tc_fence_before();
@@ -424,6 +451,7 @@ cudaError_t launch_pair(const MatmulArgs& a, const CUtensorMap& x, const CUtenso
   // every expert may end in a tile that is not full
   const long long tiles = ((a.rows + kPairN - 1) / kPairN + (a.offsets ? min((long long)a.experts, a.rows) : 0)) *
                           ((a.n + ch - 1) / ch);
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;   // more output than any device holds
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters));
   cfg.blockDim = dim3(kPairThreads);
@@ -517,7 +545,7 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.status = (int*)workspace;
   if (!encode_tiled()) return fail(cudaErrorNotSupported);
   CUtensorMap mx, mw, mu;
-  if (!map_rows(&mx, x, c.k, x_rows, ld_x, sorted_pairs ? 1 : 16) ||
+  if (!map_rows(&mx, x, c.k, x_rows, ld_x, sorted_pairs ? 1 : 128) ||
       !map_experts(&mw, a.w, c.k, c.n, c.num_experts, a.w_stride, up ? 16 : 128) ||
       !map_experts(&mu, up ? a.up : a.w, c.k, c.n, c.num_experts, up ? a.up_stride : a.w_stride, up ? 16 : 128))
     return fail(cudaErrorInvalidValue);

@@ -53,13 +53,21 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok;
 }
-// Waits for the phase, for at most `limit` SM clock cycles; false when it gave up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, long long limit) {
-  if (bar_try(bar, parity)) return true;
+// Waits for the phase, for at most `limit` SM clock cycles or until *abort is set; false when it
+// gave up. Called by whole warps: every lane gets the same answer.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* abort, long long limit) {
+  if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
   const long long t0 = clock64();
-  while (!bar_try(bar, parity))
-    if (clock64() - t0 > limit) return false;
-  return true;
+  while (true) {
+    if (__all_sync(0xffffffffu, bar_try(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort || clock64() - t0 > limit)) return false;
+  }
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p;
 }
 
 // ---- TMA loads (completion counted on `bar`; with PAIR the barrier may be the other block's) -----
