@@ -23,6 +23,8 @@ struct MatmulArgs {
   long long x_rows, ld_x, rows, ld_out, w_stride, up_stride, ws_stride, ups_stride;
   int n, k, experts, top_k, act;
   bool out_f32;
+  bool woven;      // one map reads the gate and up rows of a tile, as the tile wants them
+  bool up_first;   // ... and finds up below gate in memory
   const int8_t* x;
   const float* x_scales;
   const int* offsets;
@@ -74,8 +76,14 @@ __device__ __forceinline__ bool source_row(const MatmulArgs& a, long long i, int
   return true;
 }
 
-__device__ __forceinline__ void store_one(float* p, float y) { *p = y; }
-__device__ __forceinline__ void store_one(__nv_bfloat16* p, float y) { *p = __float2bfloat16_rn(y); }
+// Stores under a predicate: as branches they would serialise the columns (70 cycles a column).
+__device__ __forceinline__ void store_if(bool on, float* p, float y) {
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p st.global.f32 [%0], %1; }" ::"l"(p), "f"(y), "r"((uint32_t)on));
+}
+__device__ __forceinline__ void store_if(bool on, __nv_bfloat16* p, float y) {
+  const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p st.global.b16 [%0], %1; }" ::"l"(p), "h"(h), "r"((uint32_t)on));
+}
 
 // The gated activation with one fast exponential and one fast quotient: 2 + 1.2 |g| units of 2^-23
 // from the exponent's argument, and 2 from the quotient.
@@ -86,14 +94,18 @@ __device__ __forceinline__ float gated(int act, float g, float u) {
 
 // ---- many rows: pairs of blocks ------------------------------------------------------------------
 
-constexpr int kPairEpilogue = 256;  // threads that write out: two warps for each 32 channels
-constexpr int kPairThreads = 64 + kPairEpilogue;   // warp 0 loads, warp 1 issues MMAs
+// Warp 0 loads weights (and rows that lie together), warp 1 issues MMAs, warp 2 fetches the rows' factors,
+// warps 3 to 6 gather scattered rows, warps 7 to 14 write out: two for each 32 channels.
+constexpr int kGatherWarps = 4, kWriteWarps = 8, kFirstWriter = 3 + kGatherWarps;
+constexpr int kPairThreads = 32 * (kFirstWriter + kWriteWarps);
+constexpr int kGatherLag = 3;       // steps a gathered stage is given to arrive
+constexpr int kRowBox = 64;         // rows of x to a load
 constexpr int kPairStages = 6;
 constexpr int kPairN = 256;         // rows of a tile at most
 constexpr int kPairA = 128 * kStep, kPairB = (kPairN / 2) * kStep, kPairStage = kPairA + kPairB;
 
 struct PairShared {
-  uint64_t full[kPairStages], empty[kPairStages], done[2], free[2];
+  uint64_t full[kPairStages], empty[kPairStages], done[2], free[2], cols_full[2], cols_free[2];
   uint32_t tmem;
   int abort;
   int tiles[MOE_ROUTE_MAX_EXPERTS + 1];   // row tiles before each expert
@@ -101,17 +113,6 @@ struct PairShared {
   float2 cols[2][kPairN];                 // factor of a row, and whether it is written
 };
 constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + sizeof(PairShared);
-
-// Whether any thread of the epilogue says so (a barrier for them).
-__device__ __forceinline__ bool any_writer(bool v) {
-  int r;
-  asm volatile(
-      "{ .reg .pred p, q; setp.ne.s32 p, %1, 0;\n"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n"
-      "selp.s32 %0, 1, 0, q; }"
-      : "=r"(r) : "r"((int)v), "n"(kPairEpilogue) : "memory");
-  return r;
-}
 
 // Walks a cluster's tiles in order. The tiles of an expert go in bands of kBand row tiles: within a
 // band the row tiles of one channel tile come one after another, so that the clusters at work share
@@ -142,34 +143,49 @@ struct TileWalk {
 };
 
 // One warp's share of a finished tile: its 32 lanes' channels of every second chunk of 32 rows. `out`
-// points at the thread's channel of the tile's first row, `d` at the warp's lanes in tensor memory.
+// points at the thread's channel of the tile's first row, `d` at the warp's lanes in tensor memory,
+// `up` tells whether the thread's lane holds up (its partner gate, 16 lanes away) or gate.
+template <bool ACT, typename T>
+__device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* p, const int (&v)[32], const float2* cols, bool in,
+                                            bool up, float wg, float wu) {
+  const long long ld = a.ld_out;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float4 f = *(const float4*)(cols + j);
+    if constexpr (ACT) {
+      // the lane with gate takes row j, the lane with up takes row j + 1
+      const int got = __shfl_xor_sync(kFull, up ? v[j] : v[j + 1], 16);
+      const float s = up ? f.z : f.x;
+      const float g = (float)(up ? got : v[j]) * s * wg;
+      const float u = (float)(up ? v[j + 1] : got) * s * wu;
+      const float y = gated(a.act, g, u);
+      store_if(in && (up ? f.w : f.y) != 0.f, p + (up ? ld : 0), y);
+    } else {
+      store_if(in && f.y != 0.f, p, (float)v[j] * f.x * wg);
+      store_if(in && f.w != 0.f, p + ld, (float)v[j + 1] * f.z * wg);
+    }
+    p += 2 * ld;
+  }
+}
+
 template <bool ACT, typename T>
 __device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t d, const float2* cols, int live,
-                                           int first_chunk, bool in, float wg, float wu) {
-  const bool upper = threadIdx.x & 16;
-  const long long ld = a.ld_out;
-  for (int c0 = 32 * first_chunk; c0 < live; c0 += 64) {
-    int v[32];
-    __syncwarp();
-    tmem_load32(d + c0, v);
+                                           int first_chunk, bool in, bool up, float wg, float wu) {
+  // the next chunk is on its way from tensor memory while one is written
+  int v[32], w[32];
+  int c0 = 32 * first_chunk;
+  if (c0 >= live) return;
+  tmem_load32(d + c0, v);
+  for (; c0 < live; c0 += 128) {
     tmem_load_wait();
-    T* p = out + c0 * ld;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float4 f = *(const float4*)(cols + c0 + j);
-      if constexpr (ACT) {
-        // the lower half of the warp holds gate and takes row j, the upper holds up and takes row j + 1
-        const int got = __shfl_xor_sync(kFull, upper ? v[j] : v[j + 1], 16);
-        const float s = upper ? f.z : f.x;
-        const float g = (float)(upper ? got : v[j]) * s * wg;
-        const float u = (float)(upper ? v[j + 1] : got) * s * wu;
-        const float y = gated(a.act, g, u);
-        if (in && (upper ? f.w : f.y) != 0.f) store_one(p + (upper ? ld : 0), y);
-      } else {
-        if (in && f.y != 0.f) store_one(p, (float)v[j] * f.x * wg);
-        if (in && f.w != 0.f) store_one(p + ld, (float)v[j + 1] * f.z * wg);
-      }
-      p += 2 * ld;
+    if (c0 + 64 < live) tmem_load32(d + c0 + 64, w);
+    write_chunk<ACT>(a, out + c0 * a.ld_out, v, cols + c0, in, up, wg, wu);
+    __syncwarp();
+    if (c0 + 64 < live) {
+      tmem_load_wait();
+      if (c0 + 128 < live) tmem_load32(d + c0 + 128, v);
+      write_chunk<ACT>(a, out + (c0 + 64) * a.ld_out, w, cols + c0 + 64, in, up, wg, wu);
+      __syncwarp();
     }
   }
 }
@@ -192,12 +208,15 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
 
   if (tid == 0) {
     for (int s = 0; s < kPairStages; ++s) {
-      bar_init(smem_addr(&sh.full[s]), 1);
+      // the weights' (and rows') bytes, and the gather warps of both blocks
+      bar_init(smem_addr(&sh.full[s]), a.pairs ? 1 + 2 * kGatherWarps : 1);
       bar_init(smem_addr(&sh.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(smem_addr(&sh.done[b]), 1);
-      bar_init(smem_addr(&sh.free[b]), 2 * kPairEpilogue / 32);   // the epilogue warps of both blocks
+      bar_init(smem_addr(&sh.free[b]), 2 * kWriteWarps);   // the writing warps of both blocks
+      bar_init(smem_addr(&sh.cols_full[b]), 1);
+      bar_init(smem_addr(&sh.cols_free[b]), kWriteWarps);
     }
     bar_init_fence();
     sh.abort = 0;
@@ -241,17 +260,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride) {
       const int half = (live + 31) / 32 * 16;
       const int r0 = i0 + (int)rank * half;
-      int rows[4];
-      if (a.pairs) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = r0 + lane * 4 + j;
-          float unused;
-          int row = 0;
-          rows[j] = i < a.rows && source_row(a, i, row, unused) ? row : 0;
-        }
-      }
-      const uint32_t bytes = 2 * (kPairA + (a.pairs ? half : 128) * kStep);
+      const int boxes = a.pairs ? 0 : (half + kRowBox - 1) / kRowBox;
+      const uint32_t bytes = 2 * (kPairA + boxes * kRowBox * kStep);
       const int ch0 = ch * kChPair + (int)rank * kChBlock;
       for (int kb = 0; kb < k_steps; ++kb) {
         ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
@@ -259,19 +269,20 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
         const uint32_t full = of_rank(smem_addr(&sh.full[s]), 0);
         const uint32_t sa = smem_addr(base + s * kPairStage), sb = sa + kPairA;
         const int x = kb * kStep;
-        if (rank == 0 && lane == 0) bar_expect(smem_addr(&sh.full[s]), bytes);
+        if (elect()) {
+          if (rank == 0) bar_expect(smem_addr(&sh.full[s]), bytes);
+          if constexpr (ACT) {
+            if (a.woven) tma_load_5d<true>(sa, &map_w, full, x, 0, 0, ch0 / 16, walk.e);
+            else
+              for (int q = 0; q < 8; ++q)
+                tma_load_3d<true>(sa + q * 2048, (q & 1) ? &map_up : &map_w, full, x, ch0 + (q >> 1) * 16, walk.e);
+          } else {
+            tma_load_3d<true>(sa, &map_w, full, x, ch0, walk.e);
+          }
+          for (int q = 0; q < boxes; ++q)
+            tma_load_2d<true>(sb + q * kRowBox * kStep, &map_x, full, x, r0 + q * kRowBox);
+        }
         __syncwarp();
-        if constexpr (ACT) {
-          if (lane < 8)
-            tma_load_3d<true>(sa + lane * 2048, (lane & 1) ? &map_up : &map_w, full, x, ch0 + (lane >> 1) * 16, walk.e);
-        } else {
-          if (lane == 0) tma_load_3d<true>(sa, &map_w, full, x, ch0, walk.e);
-        }
-        if (a.pairs) {
-          if (lane * 4 < half) tma_gather4<true>(sb + lane * 512, &map_x, full, x, rows);
-        } else {
-          if (lane == 0) tma_load_2d<true>(sb, &map_x, full, x, r0);
-        }
         if (++s == kPairStages) {
           s = 0;
           parity ^= 1;
@@ -323,43 +334,104 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
         }
       }
     }
-  } else {
-    // ---- epilogue: this warp's 32 channels of every second 32 rows
-    const int quarter = warp & 3, first_chunk = (warp - 2) >> 2;
-    const int et = tid - 64;
+  } else if (warp == 2) {
+    // ---- factors of the tile's rows
     uint32_t tile = 0;
     TileWalk walk(first);
     int i0, live, ch;
-    for (; walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+    for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
-      float2* cols = sh.cols[b];
-      for (int c = et; c < (live + 31) / 32 * 32; c += kPairEpilogue) {
+      ok = bar_wait(smem_addr(&sh.cols_free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
+      if (!ok) break;
+#pragma unroll
+      for (int c = lane; c < kPairN; c += 32) {
         int row;
         float scale = 0.f;
         const bool real = c < live && source_row(a, i0 + c, row, scale);
-        cols[c] = make_float2(scale, real ? 1.f : 0.f);
+        sh.cols[b][c] = make_float2(scale, real ? 1.f : 0.f);
       }
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sh.cols_full[b]));
+    }
+  } else if (warp < kFirstWriter) {
+    // ---- scattered rows of x: eight threads to a row, 16 bytes each, into the swizzled tile
+    if (a.pairs) {
+      const int gt = tid - 96, chunk = gt & 7;
+      uint32_t s = 0, parity = 1, landed = 0, issued = 0;
+      auto land = [&]() {
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(of_rank(smem_addr(&sh.full[landed % kPairStages]), 0));
+        ++landed;
+      };
+      TileWalk walk(first);
+      int i0, live, ch;
+      for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride) {
+        const int half = (live + 31) / 32 * 16;
+        const int8_t* src[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = (gt >> 3) + 16 * j;
+          const long long i = (long long)i0 + (int)rank * half + r;
+          int row = 0;
+          float unused;
+          if (!(r < half && i < a.rows && source_row(a, i, row, unused))) row = 0;
+          src[j] = a.x + (size_t)row * a.ld_x + chunk * 16;
+        }
+        for (int kb = 0; kb < k_steps; ++kb) {
+          ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+          if (!ok) break;
+          const uint32_t sb = smem_addr(base + s * kPairStage) + kPairA;
+          const bool in_k = kb * kStep + chunk * 16 < a.k;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = (gt >> 3) + 16 * j;
+            if (16 * j < half)
+              copy16(sb + r * kStep + ((chunk ^ (r & 7)) << 4), in_k ? src[j] + kb * kStep : a.x, in_k);
+          }
+          copies_commit();
+          ++issued;
+          if (issued > kGatherLag) {
+            copies_wait<kGatherLag>();
+            land();
+          }
+          if (++s == kPairStages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+      }
+      copies_wait<0>();
+      while (landed < issued) land();
+    }
+  } else {
+    // ---- epilogue: this warp's 32 channels of every second 32 rows
+    const int quarter = warp & 3, first_chunk = (warp - kFirstWriter) >> 2;
+    const bool up = ACT && ((lane & 16) != 0) != a.up_first;
+    uint32_t tile = 0;
+    TileWalk walk(first);
+    int i0, live, ch;
+    for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+      const uint32_t b = tile & 1;
       const int channel = ACT ? ch * kChPair + (int)rank * kChBlock + quarter * 16 + (lane & 15)
                               : ch * kChPair + (int)rank * kChBlock + quarter * 32 + lane;
       const bool in = channel < a.n;
       const float wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)channel * 4) : 0.f;
       const float wu = ACT && in
           ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)channel * 4) : 0.f;
-      // the warps leave together: one that gave up still comes to the next tile's barrier
-      if (any_writer(!ok)) {
-        ok = false;
-        break;
-      }
-      ok = bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
-      if (ok) {
-        tc_fence_after();
-        const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
-        const size_t at = (size_t)i0 * a.ld_out + channel;
-        if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, cols, live, first_chunk, in, wg, wu);
-        else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, cols, live, first_chunk, in, wg, wu);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive_cluster(of_rank(smem_addr(&sh.free[b]), 0));
+      ok = bar_wait(smem_addr(&sh.cols_full[b]), (tile >> 1) & 1, abort, kWaitLimit) &&
+           bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
+      const size_t at = (size_t)i0 * a.ld_out + channel;
+      if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, sh.cols[b], live, first_chunk, in, up, wg, wu);
+      else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, sh.cols[b], live, first_chunk, in, up, wg, wu);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(smem_addr(&sh.cols_free[b]));
+        bar_arrive_cluster(of_rank(smem_addr(&sh.free[b]), 0));
       }
     }
   }
@@ -406,6 +478,19 @@ bool map_experts(CUtensorMap* m, const void* p, int k, int n, int experts, long 
   const cuuint64_t strides[2] = {(cuuint64_t)k, (cuuint64_t)(experts > 1 ? stride : (long long)n * k)};
   const cuuint32_t boxes[3] = {kStep, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
   return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, (void*)p, dims, strides, boxes, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The rows of two matrices woven as a tile wants them: 16 of gate, 16 of up, the next 16 of gate, ...
+// `lower` is the one at the lower address, `apart` the distance to the other.
+bool map_woven(CUtensorMap* m, const void* lower, long long apart, int k, int n, int experts, long long stride,
+               int blocks) {
+  const cuuint64_t dims[5] = {(cuuint64_t)k, 16, 2, (cuuint64_t)n / 16, (cuuint64_t)experts};
+  const cuuint64_t strides[4] = {(cuuint64_t)k, (cuuint64_t)apart, (cuuint64_t)k * 16,
+                                 (cuuint64_t)(experts > 1 ? stride : (long long)n * k)};
+  const cuuint32_t boxes[5] = {kStep, 16, 2, (cuuint32_t)blocks, 1}, ones[5] = {1, 1, 1, 1, 1};
+  return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, (void*)lower, dims, strides, boxes, ones,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -545,10 +630,21 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.status = (int*)workspace;
   if (!encode_tiled()) return fail(cudaErrorNotSupported);
   CUtensorMap mx, mw, mu;
-  if (!map_rows(&mx, x, c.k, x_rows, ld_x, sorted_pairs ? 1 : 128) ||
-      !map_experts(&mw, a.w, c.k, c.n, c.num_experts, a.w_stride, up ? 16 : 128) ||
-      !map_experts(&mu, up ? a.up : a.w, c.k, c.n, c.num_experts, up ? a.up_stride : a.w_stride, up ? 16 : 128))
+  // Gate and up of a tile in one load where the two matrices are laid out alike (one load of 128 rows
+  // against eight of 16: 447 against 338 us for 4099 rows, 2 x 8192 channels, k = 5120).
+  a.woven = a.up_first = false;
+  if (up && c.n % 16 == 0 && a.up_stride == a.w_stride && a.up != a.w) {
+    const long long apart = a.up > a.w ? a.up - a.w : a.w - a.up;
+    a.up_first = a.up < a.w;
+    a.woven = apart < (1LL << 40) &&
+              map_woven(&mw, a.up_first ? a.up : a.w, apart, c.k, c.n, c.num_experts, a.w_stride, 4);
+    if (!a.woven) a.up_first = false;
+  }
+  if (!map_rows(&mx, x, c.k, x_rows, ld_x, kRowBox) ||
+      (!a.woven && !map_experts(&mw, a.w, c.k, c.n, c.num_experts, a.w_stride, up ? 16 : 128)) ||
+      (up && !a.woven && !map_experts(&mu, a.up, c.k, c.n, c.num_experts, a.up_stride, 16)))
     return fail(cudaErrorInvalidValue);
+  if (!up || a.woven) mu = mw;
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = up ? launch_pair<true>(a, mx, mw, mu, st) : launch_pair<false>(a, mx, mw, mu, st);
   return e == cudaSuccess ? MOE_OK : fail(e);
