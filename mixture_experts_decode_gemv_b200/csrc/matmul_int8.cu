@@ -95,8 +95,8 @@ __device__ __forceinline__ float gated(int act, float g, float u) {
 // ---- many rows: pairs of blocks ------------------------------------------------------------------
 
 // Warp 0 loads weights (and rows that lie together), warp 1 issues MMAs, warp 2 fetches the rows' factors,
-// warps 3 to 6 gather scattered rows, warps 7 to 14 write out: two for each 32 channels.
-constexpr int kGatherWarps = 4, kWriteWarps = 8, kFirstWriter = 3 + kGatherWarps;
+// warps 3 to 6 gather scattered rows, warps 7 to 22 write out: four for each 32 channels.
+constexpr int kGatherWarps = 4, kWriteWarps = 16, kFirstWriter = 3 + kGatherWarps;
 constexpr int kPairThreads = 32 * (kFirstWriter + kWriteWarps);
 constexpr int kGatherLag = 3;       // steps a gathered stage is given to arrive
 constexpr int kRowBox = 64;         // rows of x to a load
@@ -142,15 +142,17 @@ struct TileWalk {
   }
 };
 
-// One warp's share of a finished tile: its 32 lanes' channels of every second chunk of 32 rows. `out`
-// points at the thread's channel of the tile's first row, `d` at the warp's lanes in tensor memory,
-// `up` tells whether the thread's lane holds up (its partner gate, 16 lanes away) or gate.
+constexpr int kChunk = 16, kChunkStep = kChunk * kWriteWarps / 4;   // rows of a warp's chunk, and to its next
+
+// One chunk of a finished tile: 16 rows of the warp's 32 channels. `p` points at the thread's channel of
+// the chunk's first row; `up` tells whether the thread's lane holds up (its partner gate, 16 lanes away)
+// or gate.
 template <bool ACT, typename T>
-__device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* p, const int (&v)[32], const float2* cols, bool in,
-                                            bool up, float wg, float wu) {
+__device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* p, const int (&v)[kChunk], const float2* cols,
+                                            bool in, bool up, float wg, float wu) {
   const long long ld = a.ld_out;
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
+  for (int j = 0; j < kChunk; j += 2) {
     const float4 f = *(const float4*)(cols + j);
     if constexpr (ACT) {
       // the lane with gate takes row j, the lane with up takes row j + 1
@@ -168,23 +170,23 @@ __device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* p, const int
   }
 }
 
+// The warp's chunks of the tile; the next one is on its way from tensor memory while one is written.
 template <bool ACT, typename T>
 __device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t d, const float2* cols, int live,
-                                           int first_chunk, bool in, bool up, float wg, float wu) {
-  // the next chunk is on its way from tensor memory while one is written
-  int v[32], w[32];
-  int c0 = 32 * first_chunk;
+                                           int c0, bool in, bool up, float wg, float wu) {
+  int v[kChunk], w[kChunk];
   if (c0 >= live) return;
-  tmem_load32(d + c0, v);
-  for (; c0 < live; c0 += 128) {
+  tmem_load16(d + c0, v);
+  for (; c0 < live; c0 += 2 * kChunkStep) {
+    const int c1 = c0 + kChunkStep, c2 = c1 + kChunkStep;
     tmem_load_wait();
-    if (c0 + 64 < live) tmem_load32(d + c0 + 64, w);
+    if (c1 < live) tmem_load16(d + c1, w);
     write_chunk<ACT>(a, out + c0 * a.ld_out, v, cols + c0, in, up, wg, wu);
     __syncwarp();
-    if (c0 + 64 < live) {
+    if (c1 < live) {
       tmem_load_wait();
-      if (c0 + 128 < live) tmem_load32(d + c0 + 128, v);
-      write_chunk<ACT>(a, out + (c0 + 64) * a.ld_out, w, cols + c0 + 64, in, up, wg, wu);
+      if (c2 < live) tmem_load16(d + c2, v);
+      write_chunk<ACT>(a, out + c1 * a.ld_out, w, cols + c1, in, up, wg, wu);
       __syncwarp();
     }
   }
@@ -405,8 +407,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       while (landed < issued) land();
     }
   } else {
-    // ---- epilogue: this warp's 32 channels of every second 32 rows
-    const int quarter = warp & 3, first_chunk = (warp - kFirstWriter) >> 2;
+    // ---- epilogue: this warp's 32 channels of every fourth 16 rows
+    const int quarter = warp & 3, first_row = ((warp - kFirstWriter) >> 2) * kChunk;
     const bool up = ACT && ((lane & 16) != 0) != a.up_first;
     uint32_t tile = 0;
     TileWalk walk(first);
@@ -425,8 +427,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       tc_fence_after();
       const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
       const size_t at = (size_t)i0 * a.ld_out + channel;
-      if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, sh.cols[b], live, first_chunk, in, up, wg, wu);
-      else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, sh.cols[b], live, first_chunk, in, up, wg, wu);
+      if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, sh.cols[b], live, first_row, in, up, wg, wu);
+      else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, sh.cols[b], live, first_row, in, up, wg, wu);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
