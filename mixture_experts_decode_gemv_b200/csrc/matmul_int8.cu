@@ -92,6 +92,69 @@ __device__ __forceinline__ float gated(int act, float g, float u) {
   return __fdividef(g * u, 1.0f + __expf(-g));
 }
 
+// The row tiles of all experts, in expert order.
+struct TileList {
+  int tiles[MOE_ROUTE_MAX_EXPERTS + 1];   // row tiles before each expert
+  int2 span[MOE_ROUTE_MAX_EXPERTS];       // its first row and its rows
+};
+
+// Fills the list (the whole block calls it; it ends with a barrier). ROWS: rows of a tile at most.
+template <int ROWS>
+__device__ __forceinline__ void list_tiles(const MatmulArgs& a, TileList& list) {
+  const int lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+    long long begin, end;
+    expert_range(a, e, begin, end);
+    list.tiles[e + 1] = (int)((end - begin + ROWS - 1) / ROWS);
+    list.span[e] = make_int2((int)begin, (int)(end - begin));
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int carry = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+      int v = e0 + lane < a.experts ? list.tiles[e0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v += u;
+      }
+      if (e0 + lane < a.experts) list.tiles[e0 + lane + 1] = v + carry;
+      carry += __shfl_sync(kFull, v, 31);
+    }
+    if (lane == 0) list.tiles[0] = 0;
+  }
+  __syncthreads();
+}
+
+// Walks a cluster's tiles in order. The tiles of an expert go in bands of kBand row tiles: within a
+// band the row tiles of one channel tile come one after another, so that the clusters at work share
+// kBand row tiles and a few channel tiles, which L2 holds.
+constexpr int kBand = 8;
+struct TileWalk {
+  int t, e = 0;
+  __device__ __forceinline__ explicit TileWalk(int first) : t(first) {}
+  // First row, rows and channel tile of tile t, and its expert in e; false behind the last. The rows of
+  // an expert are shared out in nearly equal parts, whole multiples of UNIT.
+  template <int UNIT>
+  __device__ __forceinline__ bool get(const MatmulArgs& a, const TileList& list, int ch_tiles, int& i0,
+                                      int& live, int& ch) {
+    if (t >= list.tiles[a.experts] * ch_tiles) return false;
+    while (list.tiles[e + 1] * ch_tiles <= t) ++e;
+    const int n = list.tiles[e + 1] - list.tiles[e];
+    int r = t - list.tiles[e] * ch_tiles;
+    const int band = r / (kBand * ch_tiles);
+    r -= band * kBand * ch_tiles;
+    const int wide = min(kBand, n - band * kBand);
+    ch = r / wide;
+    const int j = band * kBand + r - ch * wide;
+    const int2 span = list.span[e];
+    const int part = ((span.y - 1) / n + UNIT) & ~(UNIT - 1);
+    i0 = span.x + j * part;
+    live = min(part, span.y - j * part);
+    return true;
+  }
+};
+
 // ---- many rows: pairs of blocks ------------------------------------------------------------------
 
 // Warp 0 loads weights (and rows that lie together), warp 1 issues MMAs, warp 2 fetches the rows' factors,
@@ -108,39 +171,10 @@ struct PairShared {
   uint64_t full[kPairStages], empty[kPairStages], done[2], free[2], cols_full[2], cols_free[2];
   uint32_t tmem;
   int abort;
-  int tiles[MOE_ROUTE_MAX_EXPERTS + 1];   // row tiles before each expert
-  int2 span[MOE_ROUTE_MAX_EXPERTS];       // its first row and its rows
-  float2 cols[2][kPairN];                 // factor of a row, and whether it is written
+  TileList list;
+  float2 cols[2][kPairN];   // factor of a row, and whether it is written
 };
 constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + sizeof(PairShared);
-
-// Walks a cluster's tiles in order. The tiles of an expert go in bands of kBand row tiles: within a
-// band the row tiles of one channel tile come one after another, so that the clusters at work share
-// kBand row tiles and a few channel tiles, which L2 holds.
-constexpr int kBand = 8;
-struct TileWalk {
-  int t, e = 0;
-  __device__ __forceinline__ explicit TileWalk(int first) : t(first) {}
-  // First row, rows and channel tile of tile t, and its expert in e; false behind the last.
-  __device__ __forceinline__ bool get(const MatmulArgs& a, const PairShared& sh, int ch_tiles, int& i0,
-                                      int& live, int& ch) {
-    if (t >= sh.tiles[a.experts] * ch_tiles) return false;
-    while (sh.tiles[e + 1] * ch_tiles <= t) ++e;
-    const int n = sh.tiles[e + 1] - sh.tiles[e];
-    int r = t - sh.tiles[e] * ch_tiles;
-    const int band = r / (kBand * ch_tiles);
-    r -= band * kBand * ch_tiles;
-    const int wide = min(kBand, n - band * kBand);
-    ch = r / wide;
-    const int j = band * kBand + r - ch * wide;
-    // the expert's rows in n nearly equal parts, whole multiples of 32
-    const int2 span = sh.span[e];
-    const int part = ((span.y - 1) / n + 32) & ~31;
-    i0 = span.x + j * part;
-    live = min(part, span.y - j * part);
-    return true;
-  }
-};
 
 constexpr int kChunk = 16, kChunkStep = kChunk * kWriteWarps / 4;   // rows of a warp's chunk, and to its next
 
@@ -223,28 +257,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     bar_init_fence();
     sh.abort = 0;
   }
-  for (int e = tid; e < a.experts; e += kPairThreads) {
-    long long begin, end;
-    expert_range(a, e, begin, end);
-    sh.tiles[e + 1] = (int)((end - begin + kPairN - 1) / kPairN);
-    sh.span[e] = make_int2((int)begin, (int)(end - begin));
-  }
   if (warp == 1) tmem_alloc<2>(smem_addr(&sh.tmem), 512);
-  __syncthreads();
-  if (warp == 0) {
-    int carry = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-      int v = e0 + lane < a.experts ? sh.tiles[e0 + lane + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v += u;
-      }
-      if (e0 + lane < a.experts) sh.tiles[e0 + lane + 1] = v + carry;
-      carry += __shfl_sync(kFull, v, 31);
-    }
-    if (lane == 0) sh.tiles[0] = 0;
-  }
+  list_tiles<kPairN>(a, sh.list);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -259,7 +273,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     uint32_t s = 0, parity = 1;
     TileWalk walk(first);
     int i0, live, ch;
-    for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride) {
+    for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
       const int half = (live + 31) / 32 * 16;
       const int r0 = i0 + (int)rank * half;
       const int boxes = a.pairs ? 0 : (half + kRowBox - 1) / kRowBox;
@@ -308,7 +322,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       const uint64_t desc0 = operand_desc(smem_addr(base));
       TileWalk walk(first);
       int i0, live, ch;
-      for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+      for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
         const uint32_t b = tile & 1;
         ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
         if (!ok) break;
@@ -341,7 +355,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     uint32_t tile = 0;
     TileWalk walk(first);
     int i0, live, ch;
-    for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+    for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
       ok = bar_wait(smem_addr(&sh.cols_free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
       if (!ok) break;
@@ -368,7 +382,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       };
       TileWalk walk(first);
       int i0, live, ch;
-      for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride) {
+      for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
         const int half = (live + 31) / 32 * 16;
         const int8_t* src[8];
 #pragma unroll
@@ -413,7 +427,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     uint32_t tile = 0;
     TileWalk walk(first);
     int i0, live, ch;
-    for (; ok && walk.get(a, sh, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+    for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
       const int channel = ACT ? ch * kChPair + (int)rank * kChBlock + quarter * 16 + (lane & 15)
                               : ch * kChPair + (int)rank * kChBlock + quarter * 32 + lane;
@@ -446,6 +460,270 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
   __syncthreads();
   cluster_sync();
   if (warp == 1) tmem_free<2>(tmem, 512);
+}
+
+// ---- few rows: single blocks, k split over a cluster ----------------------------------------------
+
+// With a few rows per expert the product is one pass over the weights, so all that counts is that
+// enough of them are under way on every multiprocessor: two blocks on each, five stages of 128 channels
+// x 128 bytes (16 KB) in each. Where the tiles are fewer than the blocks, the k steps of a tile are split
+// over the blocks of a cluster, which add their int32 sums through each other's shared memory: exact in
+// any order, no workspace, nothing to clear.
+constexpr int kFewThreads = 256;    // warp 0 weights, 1 MMAs, 2 and 3 rows of x, 4 to 7 write out
+constexpr int kFewMaxCluster = 8;
+
+template <int TN>
+struct FewConfig {
+  static constexpr int kStages = TN <= 16 ? 5 : 3;
+  static constexpr int kA = 128 * kStep, kB = TN * kStep, kStage = kA + kB;
+  static constexpr int kColumns = 2 * TN;          // tensor memory: two accumulators
+  struct Shared {
+    uint64_t full[kStages], empty[kStages], done[2], free[2], red_full, red_free;
+    uint32_t tmem;
+    int abort;
+    TileList list;
+    int red[(TN + kFewMaxCluster - 1) * 128];      // sums of this block's rows from every block
+  };
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Shared);
+};
+
+__device__ __forceinline__ void store_remote(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+template <bool ACT, int TN>
+__global__ void __launch_bounds__(kFewThreads)
+matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
+                  const __grid_constant__ CUtensorMap map_up) {
+  using Config = FewConfig<TN>;
+  constexpr int kStages = Config::kStages, kStage = Config::kStage, kA = Config::kA;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  auto& sh = *(typename Config::Shared*)(base + kStages * kStage);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int split = (int)cluster_size(), rank = (int)cluster_rank();
+  constexpr int kCh = ACT ? 64 : 128;
+  const int ch_tiles = (a.n + kCh - 1) / kCh;
+  const int all_steps = (a.k + kStep - 1) / kStep;
+  const int k_first = all_steps * rank / split, k_steps = all_steps * (rank + 1) / split - k_first;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(smem_addr(&sh.full[s]), 1 + 2);     // the weights' bytes, the two row warps
+      bar_init(smem_addr(&sh.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(smem_addr(&sh.done[b]), 1);
+      bar_init(smem_addr(&sh.free[b]), 4);
+    }
+    bar_init(smem_addr(&sh.red_full), 4 * split);
+    bar_init(smem_addr(&sh.red_free), 4 * split);
+    bar_init_fence();
+    sh.abort = 0;
+  }
+  if (warp == 1) tmem_alloc<1>(smem_addr(&sh.tmem), Config::kColumns);
+  list_tiles<TN>(a, sh.list);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int first = blockIdx.x / split, stride = gridDim.x / split;
+  volatile int* abort = &sh.abort;
+  bool ok = true;
+  TileWalk walk(first);
+  int i0, live, ch;
+
+  if (warp == 0) {
+    uint32_t s = 0, parity = 1;
+    for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
+      const int ch0 = ch * kCh;
+      for (int kb = 0; kb < k_steps; ++kb) {
+        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+        if (!ok) break;
+        const uint32_t full = smem_addr(&sh.full[s]), sa = smem_addr(base + s * kStage);
+        const int x = (k_first + kb) * kStep;
+        if (elect()) {
+          bar_expect(full, kA);
+          if constexpr (ACT) {
+            if (a.woven) tma_load_5d<false>(sa, &map_w, full, x, 0, 0, ch0 / 16, walk.e);
+            else
+              for (int q = 0; q < 8; ++q)
+                tma_load_3d<false>(sa + q * 2048, (q & 1) ? &map_up : &map_w, full, x, ch0 + (q >> 1) * 16, walk.e);
+          } else {
+            tma_load_3d<false>(sa, &map_w, full, x, ch0, walk.e);
+          }
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+    }
+    // every stage has been read before the block may end
+    for (int j = 0; ok && j < kStages; ++j) {
+      ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+      if (++s == kStages) {
+        s = 0;
+        parity ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    uint32_t s = 0, parity = 0, tile = 0;
+    const uint64_t desc0 = operand_desc(smem_addr(base));
+    for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+      const uint32_t b = tile & 1;
+      ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t desc = i8_desc(128, (live + 15) & ~15);
+      const uint32_t d = tmem + b * TN;
+      for (int kb = 0; kb < k_steps; ++kb) {
+        ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, kWaitLimit);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect()) {
+          const uint64_t da = desc0 + s * (kStage >> 4), db = da + (kA >> 4);
+          mma_i8<1>(d, da, db, desc, kb > 0);
+          mma_i8<1>(d, da + 2, db + 2, desc, true);
+          mma_i8<1>(d, da + 4, db + 4, desc, true);
+          mma_i8<1>(d, da + 6, db + 6, desc, true);
+          mma_commit<1>(smem_addr(&sh.empty[s]));
+          if (kb + 1 == k_steps) mma_commit<1>(smem_addr(&sh.done[b]));
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+    }
+  } else if (warp < 4) {
+    // rows of x: eight threads to a row, 16 bytes each; rows that the tile does not have are left as
+    // they are, and so are their columns of the sums, which nothing reads
+    const int gt = tid - 64, chunk = gt & 7;
+    uint32_t s = 0, parity = 1, landed = 0, issued = 0;
+    auto land = [&]() {
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sh.full[landed % kStages]));
+      ++landed;
+    };
+    constexpr int kLag = kStages - 2;
+    for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
+      const int8_t* src[TN / 8];
+#pragma unroll
+      for (int j = 0; j < TN / 8; ++j) {
+        const int r = (gt >> 3) + 8 * j;
+        int row = 0;
+        float unused;
+        if (!(r < live && source_row(a, i0 + r, row, unused))) row = 0;
+        src[j] = a.x + (size_t)row * a.ld_x + chunk * 16;
+      }
+      for (int kb = 0; kb < k_steps; ++kb) {
+        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+        if (!ok) break;
+        const uint32_t sb = smem_addr(base + s * kStage) + kA;
+        const int at = (k_first + kb) * kStep;
+        const bool in_k = at + chunk * 16 < a.k;
+#pragma unroll
+        for (int j = 0; j < TN / 8; ++j) {
+          const int r = (gt >> 3) + 8 * j;
+          if (r < live) copy16(sb + r * kStep + ((chunk ^ (r & 7)) << 4), in_k ? src[j] + at : a.x, in_k);
+        }
+        copies_commit();
+        ++issued;
+        if (issued > kLag) {
+          copies_wait<kLag>();
+          land();
+        }
+        if (++s == kStages) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+    }
+    copies_wait<0>();
+    while (landed < issued) land();
+  } else {
+    // column c of the sums goes to block c % split, which adds it up and writes its row
+    const int quarter = warp & 3, lane_ch = quarter * 32 + lane;
+    const bool up = ACT && ((lane & 16) != 0) != a.up_first;
+    const int slots = (TN + split - 1) / split;
+    uint32_t tile = 0;
+    for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
+      const uint32_t b = tile & 1;
+      const int channel = ACT ? ch * kCh + quarter * 16 + (lane & 15) : ch * kCh + lane_ch;
+      const bool in = channel < a.n;
+      const float wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)channel * 4) : 0.f;
+      const float wu = ACT && in
+          ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)channel * 4) : 0.f;
+      // factors of this block's rows: lane l has those of slots l and l + 32
+      float factor[2] = {0.f, 0.f};
+      bool real[2] = {false, false};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = rank + (lane + 32 * j) * split;
+        int row;
+        if (lane + 32 * j < slots && c < live) real[j] = source_row(a, i0 + c, row, factor[j]);
+      }
+      ok = bar_wait(smem_addr(&sh.red_free), (tile & 1) ^ 1, abort, kWaitLimit) &&
+           bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + b * TN + ((uint32_t)(quarter * 32) << 16);
+      const uint32_t mine = smem_addr(sh.red + rank * slots * 128 + lane_ch);
+      uint32_t to = 0, at_slot = mine;
+      for (int c0 = 0; c0 < live; c0 += 16) {
+        int v[16];
+        tmem_load16(d + c0, v);
+        tmem_load_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (c0 + j < live) store_remote(of_rank(at_slot, to), v[j]);
+          if (++to == (uint32_t)split) {
+            to = 0;
+            at_slot += 128 * sizeof(int);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sh.free[b]));
+      if (lane < split) bar_arrive_release(of_rank(smem_addr(&sh.red_full), lane));
+      ok = bar_wait(smem_addr(&sh.red_full), tile & 1, abort, kWaitLimit);
+      if (!ok) break;
+      for (int q = 0, c = rank; c < live; ++q, c += split) {
+        int sum = 0;
+        for (int src = 0; src < split; ++src) sum += sh.red[(src * slots + q) * 128 + lane_ch];
+        const float f = __shfl_sync(kFull, q < 32 ? factor[0] : factor[1], q & 31);
+        const bool on = __shfl_sync(kFull, (int)(q < 32 ? real[0] : real[1]), q & 31) && in;
+        float y;
+        if constexpr (ACT) {
+          const int other = __shfl_xor_sync(kFull, sum, 16);
+          y = gated(a.act, (float)(up ? other : sum) * f * wg, (float)(up ? sum : other) * f * wu);
+        } else {
+          y = (float)sum * f * wg;
+        }
+        const size_t at = (size_t)(i0 + c) * a.ld_out + channel;
+        if (a.out_f32) store_if(on && !up, (float*)a.out + at, y);
+        else store_if(on && !up, (__nv_bfloat16*)a.out + at, y);
+      }
+      __syncwarp();
+      if (lane < split) bar_arrive_cluster(of_rank(smem_addr(&sh.red_free), lane));
+    }
+  }
+  if (!ok) {   // a wait ran out: the others are told, and the host finds it in the workspace
+    *abort = 1;
+    *a.status = MOE_ERR_DEVICE_TIMEOUT;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) tmem_free<1>(tmem, Config::kColumns);
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -497,60 +775,97 @@ bool map_woven(CUtensorMap* m, const void* lower, long long apart, int k, int n,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of two of this kernel that the device holds at once (cached per device).
-template <bool ACT>
-int pair_clusters(cudaError_t* err) {
+// Clusters of `size` blocks of the kernel that the device holds at once (cached per kernel, device, size).
+template <auto kernel>
+cudaError_t resident_clusters(int threads, size_t smem, int size, int* out) {
   static std::mutex mu;
-  static int cache[64] = {};
+  static int cache[64][kFewMaxCluster + 1] = {};
   int dev = 0;
-  *err = cudaGetDevice(&dev);
-  if (*err != cudaSuccess) return 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
-  if (dev < 0 || dev >= 64) return 0;
-  if (!cache[dev]) {
-    *err = cudaFuncSetAttribute(matmul_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
-    if (*err != cudaSuccess) return 0;
+  if (!cache[dev][size]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * 74);
-    cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    *err = cudaOccupancyMaxActiveClusters(&n, matmul_pair_kernel<ACT>, &cfg);
-    if (*err != cudaSuccess) return 0;
-    cache[dev] = n > 0 ? n : 1;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    cache[dev][size] = n > 0 ? n : 1;
   }
-  return cache[dev];
+  *out = cache[dev][size];
+  return cudaSuccess;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kernel)(P...), long long clusters, int size, int threads, size_t smem,
+                            cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)clusters * size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Tiles of a call at most: every expert may end in a tile that is not full.
+long long most_tiles(const MatmulArgs& a, int rows, int channels) {
+  const long long experts = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : 0;
+  return ((a.rows + rows - 1) / rows + experts) * ((a.n + channels - 1) / channels);
 }
 
 template <bool ACT>
 cudaError_t launch_pair(const MatmulArgs& a, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& up,
                         cudaStream_t st) {
-  cudaError_t e;
-  const int clusters = pair_clusters<ACT>(&e);
+  int clusters = 0;
+  const cudaError_t e = resident_clusters<matmul_pair_kernel<ACT>>(kPairThreads, kPairSmem, 2, &clusters);
   if (e != cudaSuccess) return e;
-  const int ch = ACT ? 128 : 256;
-  // every expert may end in a tile that is not full
-  const long long tiles = ((a.rows + kPairN - 1) / kPairN + (a.offsets ? min((long long)a.experts, a.rows) : 0)) *
-                          ((a.n + ch - 1) / ch);
+  const long long tiles = most_tiles(a, kPairN, ACT ? 128 : 256);
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;   // more output than any device holds
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (unsigned)(tiles < clusters ? tiles : clusters));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = kPairSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, matmul_pair_kernel<ACT>, a, x, w, up);
+  return launch_clusters(matmul_pair_kernel<ACT>, tiles < clusters ? tiles : clusters, 2, kPairThreads, kPairSmem, st,
+                         a, x, w, up);
+}
+
+template <bool ACT, int TN>
+cudaError_t launch_few(const MatmulArgs& a, const CUtensorMap& w, const CUtensorMap& up, cudaStream_t st) {
+  constexpr size_t smem = FewConfig<TN>::kSmem;
+  const long long tiles = most_tiles(a, TN, ACT ? 64 : 128);
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int steps = (a.k + kStep - 1) / kStep;
+  // the largest split whose clusters all run at once
+  int size = steps < kFewMaxCluster ? steps : kFewMaxCluster, clusters = 0;
+  for (; size >= 1; --size) {
+    const cudaError_t e = resident_clusters<matmul_few_kernel<ACT, TN>>(kFewThreads, smem, size, &clusters);
+    if (e != cudaSuccess) return e;
+    if (size == 1 || tiles <= clusters) break;
+  }
+  return launch_clusters(matmul_few_kernel<ACT, TN>, tiles < clusters ? tiles : clusters, size, kFewThreads, smem, st,
+                         a, w, up);
+}
+
+template <bool ACT>
+cudaError_t launch_product(const MatmulArgs& a, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& up,
+                           cudaStream_t st) {
+  const long long per = a.rows / (a.offsets ? a.experts : 1);   // rows of an expert, if they were even
+  if (a.rows <= 16 || per <= 8) return launch_few<ACT, 16>(a, w, up, st);
+  if (per <= 64) return launch_few<ACT, 64>(a, w, up, st);
+  return launch_pair<ACT>(a, x, w, up, st);
 }
 
 int check_cfg(const moe_matmul_cfg* c, int64_t rows) {
@@ -648,6 +963,6 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
     return fail(cudaErrorInvalidValue);
   if (!up || a.woven) mu = mw;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = up ? launch_pair<true>(a, mx, mw, mu, st) : launch_pair<false>(a, mx, mw, mu, st);
+  const cudaError_t e = up ? launch_product<true>(a, mx, mw, mu, st) : launch_product<false>(a, mx, mw, mu, st);
   return e == cudaSuccess ? MOE_OK : fail(e);
 }
