@@ -158,17 +158,17 @@ struct TileWalk {
 // ---- many rows: pairs of blocks ------------------------------------------------------------------
 
 // Warp 0 loads weights (and rows that lie together), warp 1 issues MMAs, warp 2 fetches the rows' factors,
-// warps 3 to 6 gather scattered rows, warps 7 to 22 write out: four for each 32 channels.
-constexpr int kGatherWarps = 4, kWriteWarps = 16, kFirstWriter = 3 + kGatherWarps;
+// warp 3 tells the first block which gathered stages have landed, warps 4 to 7 gather scattered rows, warps
+// 8 to 23 write out: four for each 32 channels.
+constexpr int kGatherWarps = 4, kWriteWarps = 16, kFirstGather = 4, kFirstWriter = kFirstGather + kGatherWarps;
 constexpr int kPairThreads = 32 * (kFirstWriter + kWriteWarps);
-constexpr int kGatherLag = 3;       // steps a gathered stage is given to arrive
 constexpr int kRowBox = 64;         // rows of x to a load
 constexpr int kPairStages = 6;
 constexpr int kPairN = 256;         // rows of a tile at most
 constexpr int kPairA = 128 * kStep, kPairB = (kPairN / 2) * kStep, kPairStage = kPairA + kPairB;
 
 struct PairShared {
-  uint64_t full[kPairStages], empty[kPairStages], done[2], free[2], cols_full[2], cols_free[2];
+  uint64_t full[kPairStages], empty[kPairStages], landed[kPairStages], done[2], free[2], cols_full[2], cols_free[2];
   uint32_t tmem;
   int abort;
   TileList list;
@@ -244,8 +244,9 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
 
   if (tid == 0) {
     for (int s = 0; s < kPairStages; ++s) {
-      // the weights' (and rows') bytes, and the gather warps of both blocks
-      bar_init(smem_addr(&sh.full[s]), a.pairs ? 1 + 2 * kGatherWarps : 1);
+      // the weights' (and rows') bytes, and gathered rows of both blocks
+      bar_init(smem_addr(&sh.full[s]), a.pairs ? 1 + 2 : 1);
+      bar_init(smem_addr(&sh.landed[s]), 32 * kGatherWarps);
       bar_init(smem_addr(&sh.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -258,6 +259,13 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     sh.abort = 0;
   }
   if (warp == 1) tmem_alloc<2>(smem_addr(&sh.tmem), 512);
+  if (warp == 0 && elect()) {
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+    prefetch_map(&map_up);
+  }
+  release_next();
+  wait_previous();
   list_tiles<kPairN>(a, sh.list);
   tc_fence_before();
   __syncthreads();
@@ -369,17 +377,30 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&sh.cols_full[b]));
     }
+  } else if (warp == 3) {
+    // ---- a gathered stage has landed: the first block hears of it, after the proxy fence
+    if (a.pairs) {
+      uint32_t s = 0, parity = 0;
+      TileWalk walk(first);
+      int i0, live, ch;
+      for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride)
+        for (int kb = 0; kb < k_steps; ++kb) {
+          ok = bar_wait(smem_addr(&sh.landed[s]), parity, abort, kWaitLimit);
+          if (!ok) break;
+          fence_async_proxy();
+          if (elect()) bar_arrive_cluster(of_rank(smem_addr(&sh.full[s]), 0));
+          __syncwarp();
+          if (++s == kPairStages) {
+            s = 0;
+            parity ^= 1;
+          }
+        }
+    }
   } else if (warp < kFirstWriter) {
     // ---- scattered rows of x: eight threads to a row, 16 bytes each, into the swizzled tile
     if (a.pairs) {
-      const int gt = tid - 96, chunk = gt & 7;
-      uint32_t s = 0, parity = 1, landed = 0, issued = 0;
-      auto land = [&]() {
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) bar_arrive_cluster(of_rank(smem_addr(&sh.full[landed % kPairStages]), 0));
-        ++landed;
-      };
+      const int gt = tid - 32 * kFirstGather, chunk = gt & 7;
+      uint32_t s = 0, parity = 1;
       TileWalk walk(first);
       int i0, live, ch;
       for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
@@ -405,20 +426,14 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
             if (16 * j < half)
               copy16(sb + r * kStep + ((chunk ^ (r & 7)) << 4), in_k ? src[j] + kb * kStep : a.x, in_k);
           }
-          copies_commit();
-          ++issued;
-          if (issued > kGatherLag) {
-            copies_wait<kGatherLag>();
-            land();
-          }
+          copies_arrive(smem_addr(&sh.landed[s]));
           if (++s == kPairStages) {
             s = 0;
             parity ^= 1;
           }
         }
       }
-      copies_wait<0>();
-      while (landed < issued) land();
+      copies_wait_all();
     }
   } else {
     // ---- epilogue: this warp's 32 channels of every fourth 16 rows
@@ -474,7 +489,7 @@ constexpr int kFewMaxCluster = 8;
 
 template <int TN>
 struct FewConfig {
-  static constexpr int kStages = TN <= 16 ? 5 : 3;
+  static constexpr int kStages = TN == 16 ? 5 : TN == 32 ? 4 : 7;
   static constexpr int kA = 128 * kStep, kB = TN * kStep, kStage = kA + kB;
   static constexpr int kColumns = 2 * TN;          // tensor memory: two accumulators
   struct Shared {
@@ -482,6 +497,7 @@ struct FewConfig {
     uint32_t tmem;
     int abort;
     TileList list;
+    float2 cols[4][TN];                            // factors of the rows, a copy for each writing warp
     int red[(TN + kFewMaxCluster - 1) * 128];      // sums of this block's rows from every block
   };
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Shared);
@@ -509,7 +525,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(smem_addr(&sh.full[s]), 1 + 2);     // the weights' bytes, the two row warps
+      bar_init(smem_addr(&sh.full[s]), 1 + 64);     // the weights' bytes, the threads that copy rows
       bar_init(smem_addr(&sh.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -522,6 +538,12 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     sh.abort = 0;
   }
   if (warp == 1) tmem_alloc<1>(smem_addr(&sh.tmem), Config::kColumns);
+  if (warp == 0 && elect()) {
+    prefetch_map(&map_w);
+    prefetch_map(&map_up);
+  }
+  release_next();
+  wait_previous();
   list_tiles<TN>(a, sh.list);
   tc_fence_before();
   __syncthreads();
@@ -582,6 +604,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       for (int kb = 0; kb < k_steps; ++kb) {
         ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, kWaitLimit);
         if (!ok) break;
+        fence_async_proxy();
         tc_fence_after();
         if (elect()) {
           const uint64_t da = desc0 + s * (kStage >> 4), db = da + (kA >> 4);
@@ -603,14 +626,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     // rows of x: eight threads to a row, 16 bytes each; rows that the tile does not have are left as
     // they are, and so are their columns of the sums, which nothing reads
     const int gt = tid - 64, chunk = gt & 7;
-    uint32_t s = 0, parity = 1, landed = 0, issued = 0;
-    auto land = [&]() {
-      fence_async_proxy();
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&sh.full[landed % kStages]));
-      ++landed;
-    };
-    constexpr int kLag = kStages - 2;
+    uint32_t s = 0, parity = 1;
     for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
       const int8_t* src[TN / 8];
 #pragma unroll
@@ -632,20 +648,14 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
           const int r = (gt >> 3) + 8 * j;
           if (r < live) copy16(sb + r * kStep + ((chunk ^ (r & 7)) << 4), in_k ? src[j] + at : a.x, in_k);
         }
-        copies_commit();
-        ++issued;
-        if (issued > kLag) {
-          copies_wait<kLag>();
-          land();
-        }
+        copies_arrive(smem_addr(&sh.full[s]));
         if (++s == kStages) {
           s = 0;
           parity ^= 1;
         }
       }
     }
-    copies_wait<0>();
-    while (landed < issued) land();
+    copies_wait_all();
   } else {
     // column c of the sums goes to block c % split, which adds it up and writes its row
     const int quarter = warp & 3, lane_ch = quarter * 32 + lane;
@@ -659,20 +669,36 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       const float wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)channel * 4) : 0.f;
       const float wu = ACT && in
           ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)channel * 4) : 0.f;
-      // factors of this block's rows: lane l has those of slots l and l + 32
-      float factor[2] = {0.f, 0.f};
-      bool real[2] = {false, false};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = rank + (lane + 32 * j) * split;
+      // factors of the rows that this block writes: slot q is row rank + q * split
+      float2* cols = sh.cols[quarter];
+      for (int q = lane; q < (slots + 15) / 16 * 16; q += 32) {
+        const int c = rank + q * split;
         int row;
-        if (lane + 32 * j < slots && c < live) real[j] = source_row(a, i0 + c, row, factor[j]);
+        float scale = 0.f;
+        const bool real = c < live && source_row(a, i0 + c, row, scale);
+        cols[q] = make_float2(scale, real ? 1.f : 0.f);
       }
-      ok = bar_wait(smem_addr(&sh.red_free), (tile & 1) ^ 1, abort, kWaitLimit) &&
+      __syncwarp();
+      ok = (split == 1 || bar_wait(smem_addr(&sh.red_free), (tile & 1) ^ 1, abort, kWaitLimit)) &&
            bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * TN + ((uint32_t)(quarter * 32) << 16);
+      if (split == 1) {
+        for (int c0 = 0; c0 < live; c0 += 16) {
+          int v[16];
+          tmem_load16(d + c0, v);
+          tmem_load_wait();
+          const size_t at = (size_t)(i0 + c0) * a.ld_out + channel;
+          if (a.out_f32) write_chunk<ACT>(a, (float*)a.out + at, v, cols + c0, in, up, wg, wu);
+          else write_chunk<ACT>(a, (__nv_bfloat16*)a.out + at, v, cols + c0, in, up, wg, wu);
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&sh.free[b]));
+        continue;
+      }
       const uint32_t mine = smem_addr(sh.red + rank * slots * 128 + lane_ch);
       uint32_t to = 0, at_slot = mine;
       for (int c0 = 0; c0 < live; c0 += 16) {
@@ -695,21 +721,28 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       if (lane < split) bar_arrive_release(of_rank(smem_addr(&sh.red_full), lane));
       ok = bar_wait(smem_addr(&sh.red_full), tile & 1, abort, kWaitLimit);
       if (!ok) break;
-      for (int q = 0, c = rank; c < live; ++q, c += split) {
-        int sum = 0;
-        for (int src = 0; src < split; ++src) sum += sh.red[(src * slots + q) * 128 + lane_ch];
-        const float f = __shfl_sync(kFull, q < 32 ? factor[0] : factor[1], q & 31);
-        const bool on = __shfl_sync(kFull, (int)(q < 32 ? real[0] : real[1]), q & 31) && in;
-        float y;
-        if constexpr (ACT) {
-          const int other = __shfl_xor_sync(kFull, sum, 16);
-          y = gated(a.act, (float)(up ? other : sum) * f * wg, (float)(up ? sum : other) * f * wu);
-        } else {
-          y = (float)sum * f * wg;
+      // four rows at a time, so that their loads and exponentials overlap
+      for (int q = 0, c = rank; c < live; q += 4, c += 4 * split) {
+        int sum[4] = {0, 0, 0, 0};
+        for (int src = 0; src < split; ++src)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (q + j < slots) sum[j] += sh.red[(src * slots + q + j) * 128 + lane_ch];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = cols[q + j];
+          float y;
+          if constexpr (ACT) {
+            const int other = __shfl_xor_sync(kFull, sum[j], 16);
+            y = gated(a.act, (float)(up ? other : sum[j]) * f.x * wg, (float)(up ? sum[j] : other) * f.x * wu);
+          } else {
+            y = (float)sum[j] * f.x * wg;
+          }
+          const bool on = in && !up && q + j < slots && c + j * split < live && f.y != 0.f;
+          const size_t at = (size_t)(i0 + c + j * split) * a.ld_out + channel;
+          if (a.out_f32) store_if(on, (float*)a.out + at, y);
+          else store_if(on, (__nv_bfloat16*)a.out + at, y);
         }
-        const size_t at = (size_t)(i0 + c) * a.ld_out + channel;
-        if (a.out_f32) store_if(on && !up, (float*)a.out + at, y);
-        else store_if(on && !up, (__nv_bfloat16*)a.out + at, y);
       }
       __syncwarp();
       if (lane < split) bar_arrive_cluster(of_rank(smem_addr(&sh.red_free), lane));
@@ -815,12 +848,14 @@ cudaError_t launch_clusters(void (*kernel)(P...), long long clusters, int size, 
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = size;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -864,6 +899,7 @@ cudaError_t launch_product(const MatmulArgs& a, const CUtensorMap& x, const CUte
                            cudaStream_t st) {
   const long long per = a.rows / (a.offsets ? a.experts : 1);   // rows of an expert, if they were even
   if (a.rows <= 16 || per <= 8) return launch_few<ACT, 16>(a, w, up, st);
+  if (per <= 24) return launch_few<ACT, 32>(a, w, up, st);
   if (per <= 64) return launch_few<ACT, 64>(a, w, up, st);
   return launch_pair<ACT>(a, x, w, up, st);
 }
