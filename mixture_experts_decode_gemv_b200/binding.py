@@ -176,10 +176,12 @@ def _ptr(a) -> Optional[int]:
     """Device or host address of ``a``: None, an int, a torch tensor or a numpy array."""
     if a is None:
         return None
+    try:
+        return a.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(a, int):
         return a
-    if hasattr(a, "data_ptr"):
-        return a.data_ptr()
     if isinstance(a, np.ndarray):
         if not a.flags["C_CONTIGUOUS"]:
             raise ValueError("host arrays must be C-contiguous")

@@ -6,7 +6,7 @@
 // The sums are int32 and exact (|x|, |w| <= 128 and k <= 131056 keep them below 2^31), so neither
 // tiling nor order can change a bit of them; what follows is float32 and one rounding to the output
 // type.
-#include <mutex>
+#include <atomic>
 
 #include <cuda.h>
 
@@ -480,42 +480,39 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
 // ---- few rows: single blocks, k split over a cluster ----------------------------------------------
 
 // With a few rows per expert the product is one pass over the weights, so all that counts is that
-// enough of them are under way on every multiprocessor: two blocks on each, five stages of 128 channels
-// x 128 bytes (16 KB) in each. Where the tiles are fewer than the blocks, the k steps of a tile are split
-// over the blocks of a cluster, which add their int32 sums through each other's shared memory: exact in
-// any order, no workspace, nothing to clear.
+// enough of them are under way on every multiprocessor: seven stages of 128 channels x 128 bytes (16 KB).
+// Where the tiles are fewer than the blocks, the k steps of a tile are split over the blocks of a cluster,
+// which add their int32 sums through each other's shared memory: exact in any order, no workspace, nothing
+// to clear. (Two blocks of 16 or 32 rows and five or four stages on a multiprocessor took 46.5 and 49.0 us
+// against 45.9 for one of 64 rows and seven, 16 rows x 8 of 128 experts, 2 x 768 channels, k = 2048; 61.4
+// and 64.3 against 61.2 with 64 rows.)
 constexpr int kFewThreads = 256;    // warp 0 weights, 1 MMAs, 2 and 3 rows of x, 4 to 7 write out
 constexpr int kFewMaxCluster = 8;
+constexpr int kFewStages = 7;
+constexpr int kFewN = 64;           // rows of a tile at most
+constexpr int kFewA = 128 * kStep, kFewB = kFewN * kStep, kFewStage = kFewA + kFewB;
 
-template <int TN>
-struct FewConfig {
-  static constexpr int kStages = TN == 16 ? 5 : TN == 32 ? 4 : 7;
-  static constexpr int kA = 128 * kStep, kB = TN * kStep, kStage = kA + kB;
-  static constexpr int kColumns = 2 * TN;          // tensor memory: two accumulators
-  struct Shared {
-    uint64_t full[kStages], empty[kStages], done[2], free[2], red_full, red_free;
-    uint32_t tmem;
-    int abort;
-    TileList list;
-    float2 cols[4][TN];                            // factors of the rows, a copy for each writing warp
-    int red[(TN + kFewMaxCluster - 1) * 128];      // sums of this block's rows from every block
-  };
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + sizeof(Shared);
+struct FewShared {
+  uint64_t full[kFewStages], empty[kFewStages], done[2], free[2], red_full, red_free;
+  uint32_t tmem;
+  int abort;
+  TileList list;
+  float2 cols[4][kFewN];                            // factors of the rows, a copy for each writing warp
+  int red[(kFewN + kFewMaxCluster - 1) * 128];      // sums of this block's rows from every block
 };
+constexpr size_t kFewSmem = 1024 + (size_t)kFewStages * kFewStage + sizeof(FewShared);
 
 __device__ __forceinline__ void store_remote(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-template <bool ACT, int TN>
-__global__ void __launch_bounds__(kFewThreads)
+template <bool ACT>
+__global__ void __launch_bounds__(kFewThreads, 1)
 matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_up) {
-  using Config = FewConfig<TN>;
-  constexpr int kStages = Config::kStages, kStage = Config::kStage, kA = Config::kA;
   extern __shared__ uint8_t raw[];
   uint8_t* base = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  auto& sh = *(typename Config::Shared*)(base + kStages * kStage);
+  FewShared& sh = *(FewShared*)(base + kFewStages * kFewStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int split = (int)cluster_size(), rank = (int)cluster_rank();
   constexpr int kCh = ACT ? 64 : 128;
@@ -524,7 +521,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
   const int k_first = all_steps * rank / split, k_steps = all_steps * (rank + 1) / split - k_first;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kFewStages; ++s) {
       bar_init(smem_addr(&sh.full[s]), 1 + 64);     // the weights' bytes, the threads that copy rows
       bar_init(smem_addr(&sh.empty[s]), 1);
     }
@@ -537,14 +534,14 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     bar_init_fence();
     sh.abort = 0;
   }
-  if (warp == 1) tmem_alloc<1>(smem_addr(&sh.tmem), Config::kColumns);
+  if (warp == 1) tmem_alloc<1>(smem_addr(&sh.tmem), 2 * kFewN);
   if (warp == 0 && elect()) {
     prefetch_map(&map_w);
     prefetch_map(&map_up);
   }
   release_next();
   wait_previous();
-  list_tiles<TN>(a, sh.list);
+  list_tiles<kFewN>(a, sh.list);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -563,10 +560,10 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       for (int kb = 0; kb < k_steps; ++kb) {
         ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
         if (!ok) break;
-        const uint32_t full = smem_addr(&sh.full[s]), sa = smem_addr(base + s * kStage);
+        const uint32_t full = smem_addr(&sh.full[s]), sa = smem_addr(base + s * kFewStage);
         const int x = (k_first + kb) * kStep;
         if (elect()) {
-          bar_expect(full, kA);
+          bar_expect(full, kFewA);
           if constexpr (ACT) {
             if (a.woven) tma_load_5d<false>(sa, &map_w, full, x, 0, 0, ch0 / 16, walk.e);
             else
@@ -577,16 +574,16 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
           }
         }
         __syncwarp();
-        if (++s == kStages) {
+        if (++s == kFewStages) {
           s = 0;
           parity ^= 1;
         }
       }
     }
     // every stage has been read before the block may end
-    for (int j = 0; ok && j < kStages; ++j) {
+    for (int j = 0; ok && j < kFewStages; ++j) {
       ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
-      if (++s == kStages) {
+      if (++s == kFewStages) {
         s = 0;
         parity ^= 1;
       }
@@ -600,14 +597,14 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       if (!ok) break;
       tc_fence_after();
       const uint32_t desc = i8_desc(128, (live + 15) & ~15);
-      const uint32_t d = tmem + b * TN;
+      const uint32_t d = tmem + b * kFewN;
       for (int kb = 0; kb < k_steps; ++kb) {
         ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, kWaitLimit);
         if (!ok) break;
         fence_async_proxy();
         tc_fence_after();
         if (elect()) {
-          const uint64_t da = desc0 + s * (kStage >> 4), db = da + (kA >> 4);
+          const uint64_t da = desc0 + s * (kFewStage >> 4), db = da + (kFewA >> 4);
           mma_i8<1>(d, da, db, desc, kb > 0);
           mma_i8<1>(d, da + 2, db + 2, desc, true);
           mma_i8<1>(d, da + 4, db + 4, desc, true);
@@ -616,7 +613,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
           if (kb + 1 == k_steps) mma_commit<1>(smem_addr(&sh.done[b]));
         }
         __syncwarp();
-        if (++s == kStages) {
+        if (++s == kFewStages) {
           s = 0;
           parity ^= 1;
         }
@@ -628,9 +625,9 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     const int gt = tid - 64, chunk = gt & 7;
     uint32_t s = 0, parity = 1;
     for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
-      const int8_t* src[TN / 8];
+      const int8_t* src[kFewN / 8];
 #pragma unroll
-      for (int j = 0; j < TN / 8; ++j) {
+      for (int j = 0; j < kFewN / 8; ++j) {
         const int r = (gt >> 3) + 8 * j;
         int row = 0;
         float unused;
@@ -640,16 +637,16 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       for (int kb = 0; kb < k_steps; ++kb) {
         ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
         if (!ok) break;
-        const uint32_t sb = smem_addr(base + s * kStage) + kA;
+        const uint32_t sb = smem_addr(base + s * kFewStage) + kFewA;
         const int at = (k_first + kb) * kStep;
         const bool in_k = at + chunk * 16 < a.k;
 #pragma unroll
-        for (int j = 0; j < TN / 8; ++j) {
+        for (int j = 0; j < kFewN / 8; ++j) {
           const int r = (gt >> 3) + 8 * j;
           if (r < live) copy16(sb + r * kStep + ((chunk ^ (r & 7)) << 4), in_k ? src[j] + at : a.x, in_k);
         }
         copies_arrive(smem_addr(&sh.full[s]));
-        if (++s == kStages) {
+        if (++s == kFewStages) {
           s = 0;
           parity ^= 1;
         }
@@ -660,7 +657,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     // column c of the sums goes to block c % split, which adds it up and writes its row
     const int quarter = warp & 3, lane_ch = quarter * 32 + lane;
     const bool up = ACT && ((lane & 16) != 0) != a.up_first;
-    const int slots = (TN + split - 1) / split;
+    const int slots = (kFewN + split - 1) / split;
     uint32_t tile = 0;
     for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
@@ -683,7 +680,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
            bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem + b * TN + ((uint32_t)(quarter * 32) << 16);
+      const uint32_t d = tmem + b * kFewN + ((uint32_t)(quarter * 32) << 16);
       if (split == 1) {
         for (int c0 = 0; c0 < live; c0 += 16) {
           int v[16];
@@ -756,7 +753,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 1) tmem_free<1>(tmem, Config::kColumns);
+  if (warp == 1) tmem_free<1>(tmem, 2 * kFewN);
 }
 
 // ---- host ----------------------------------------------------------------------------------------
@@ -808,18 +805,14 @@ bool map_woven(CUtensorMap* m, const void* lower, long long apart, int k, int n,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of `size` blocks of the kernel that the device holds at once (cached per kernel, device, size).
+// Clusters of `size` blocks of the kernel that device `dev` holds at once (cached per kernel, device, size).
 template <auto kernel>
-cudaError_t resident_clusters(int threads, size_t smem, int size, int* out) {
-  static std::mutex mu;
-  static int cache[64][kFewMaxCluster + 1] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
+cudaError_t resident_clusters(int dev, int threads, size_t smem, int size, int* out) {
+  static std::atomic<int> cache[64][kFewMaxCluster + 1] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!cache[dev][size]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  int n = cache[dev][size].load(std::memory_order_acquire);
+  if (!n) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(size);
@@ -831,12 +824,12 @@ cudaError_t resident_clusters(int threads, size_t smem, int size, int* out) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
-    cache[dev][size] = n > 0 ? n : 1;
+    if (n < 1) n = 1;
+    cache[dev][size].store(n, std::memory_order_release);
   }
-  *out = cache[dev][size];
+  *out = n;
   return cudaSuccess;
 }
 
@@ -865,43 +858,59 @@ long long most_tiles(const MatmulArgs& a, int rows, int channels) {
   return ((a.rows + rows - 1) / rows + experts) * ((a.n + channels - 1) / channels);
 }
 
+// The tensor maps of a call; only those that its kernel reads are made.
+struct Maps {
+  CUtensorMap x, w, up;
+};
+
 template <bool ACT>
-cudaError_t launch_pair(const MatmulArgs& a, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& up,
-                        cudaStream_t st) {
-  int clusters = 0;
-  const cudaError_t e = resident_clusters<matmul_pair_kernel<ACT>>(kPairThreads, kPairSmem, 2, &clusters);
+cudaError_t launch_product(MatmulArgs& a, cudaStream_t st) {
+  int dev = 0, pairs = 0, clusters = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const long long tiles = most_tiles(a, kPairN, ACT ? 128 : 256);
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;   // more output than any device holds
-  return launch_clusters(matmul_pair_kernel<ACT>, tiles < clusters ? tiles : clusters, 2, kPairThreads, kPairSmem, st,
-                         a, x, w, up);
-}
-
-template <bool ACT, int TN>
-cudaError_t launch_few(const MatmulArgs& a, const CUtensorMap& w, const CUtensorMap& up, cudaStream_t st) {
-  constexpr size_t smem = FewConfig<TN>::kSmem;
-  const long long tiles = most_tiles(a, TN, ACT ? 64 : 128);
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const int steps = (a.k + kStep - 1) / kStep;
-  // the largest split whose clusters all run at once
-  int size = steps < kFewMaxCluster ? steps : kFewMaxCluster, clusters = 0;
-  for (; size >= 1; --size) {
-    const cudaError_t e = resident_clusters<matmul_few_kernel<ACT, TN>>(kFewThreads, smem, size, &clusters);
-    if (e != cudaSuccess) return e;
-    if (size == 1 || tiles <= clusters) break;
+  e = resident_clusters<matmul_pair_kernel<ACT>>(dev, kPairThreads, kPairSmem, 2, &pairs);
+  if (e != cudaSuccess) return e;
+  Maps m;
+  // Gate and up of a tile in one load where the two matrices are laid out alike (one load of 128 rows
+  // against eight of 16: 308 against 237 us for 4099 rows, 2 x 8192 channels, k = 5120).
+  a.woven = a.up_first = false;
+  if (ACT && a.n % 16 == 0 && a.up_stride == a.w_stride && a.up != a.w) {
+    const long long apart = a.up > a.w ? a.up - a.w : a.w - a.up;
+    a.up_first = a.up < a.w;
+    a.woven = apart < (1LL << 40) &&
+              map_woven(&m.w, a.up_first ? a.up : a.w, apart, a.k, a.n, a.experts, a.w_stride, 4);
+    if (!a.woven) a.up_first = false;
   }
-  return launch_clusters(matmul_few_kernel<ACT, TN>, tiles < clusters ? tiles : clusters, size, kFewThreads, smem, st,
-                         a, w, up);
-}
+  if (!a.woven && !map_experts(&m.w, a.w, a.k, a.n, a.experts, a.w_stride, ACT ? 16 : 128)) return cudaErrorInvalidValue;
+  if (ACT && !a.woven) {
+    if (!map_experts(&m.up, a.up, a.k, a.n, a.experts, a.up_stride, 16)) return cudaErrorInvalidValue;
+  } else {
+    m.up = m.w;
+  }
 
-template <bool ACT>
-cudaError_t launch_product(const MatmulArgs& a, const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& up,
-                           cudaStream_t st) {
+  // Few rows: where an expert has about 16 rows or fewer (128 experts, 2 x 768 channels, k = 2048: 46, 61, 71,
+  // 77, 89 us with 1, 4, 8, 16, 32 rows an expert, against 50, 65, 75, 77, 80 in pairs), and up to one tile's
+  // 64 where the pairs' tiles would leave half of the device idle (64 rows, 5120 channels, k = 8192: 14.4
+  // against 18.1; 2 x 8192 channels, k = 5120, which fill it: 19.4 against 18.0).
   const long long per = a.rows / (a.offsets ? a.experts : 1);   // rows of an expert, if they were even
-  if (a.rows <= 16 || per <= 8) return launch_few<ACT, 16>(a, w, up, st);
-  if (per <= 24) return launch_few<ACT, 32>(a, w, up, st);
-  if (per <= 64) return launch_few<ACT, 64>(a, w, up, st);
-  return launch_pair<ACT>(a, x, w, up, st);
+  const long long pair_tiles = most_tiles(a, kPairN, ACT ? 128 : 256), few_tiles = most_tiles(a, kFewN, ACT ? 64 : 128);
+  if (pair_tiles > 0x7fffffffLL || few_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;   // more output than any device holds
+  if (per <= 16 || (per <= kFewN && 2 * pair_tiles <= pairs)) {
+    const int steps = (a.k + kStep - 1) / kStep;
+    // the largest split whose clusters all run at once
+    int size = steps < kFewMaxCluster ? steps : kFewMaxCluster;
+    for (; size >= 1; --size) {
+      e = resident_clusters<matmul_few_kernel<ACT>>(dev, kFewThreads, kFewSmem, size, &clusters);
+      if (e != cudaSuccess) return e;
+      if (size == 1 || few_tiles <= clusters) break;
+    }
+    return launch_clusters(matmul_few_kernel<ACT>, few_tiles < clusters ? few_tiles : clusters, size, kFewThreads,
+                           kFewSmem, st, a, m.w, m.up);
+  }
+  if (a.pairs) m.x = m.w;   // gathered rows go without a map
+  else if (!map_rows(&m.x, a.x, a.k, a.x_rows, a.ld_x, kRowBox)) return cudaErrorInvalidValue;
+  return launch_clusters(matmul_pair_kernel<ACT>, pair_tiles < pairs ? pair_tiles : pairs, 2, kPairThreads, kPairSmem,
+                         st, a, m.x, m.w, m.up);
 }
 
 int check_cfg(const moe_matmul_cfg* c, int64_t rows) {
@@ -982,23 +991,7 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.out = out;
   a.status = (int*)workspace;
   if (!encode_tiled()) return fail(cudaErrorNotSupported);
-  CUtensorMap mx, mw, mu;
-  // Gate and up of a tile in one load where the two matrices are laid out alike (one load of 128 rows
-  // against eight of 16: 447 against 338 us for 4099 rows, 2 x 8192 channels, k = 5120).
-  a.woven = a.up_first = false;
-  if (up && c.n % 16 == 0 && a.up_stride == a.w_stride && a.up != a.w) {
-    const long long apart = a.up > a.w ? a.up - a.w : a.w - a.up;
-    a.up_first = a.up < a.w;
-    a.woven = apart < (1LL << 40) &&
-              map_woven(&mw, a.up_first ? a.up : a.w, apart, c.k, c.n, c.num_experts, a.w_stride, 4);
-    if (!a.woven) a.up_first = false;
-  }
-  if (!map_rows(&mx, x, c.k, x_rows, ld_x, kRowBox) ||
-      (!a.woven && !map_experts(&mw, a.w, c.k, c.n, c.num_experts, a.w_stride, up ? 16 : 128)) ||
-      (up && !a.woven && !map_experts(&mu, a.up, c.k, c.n, c.num_experts, a.up_stride, 16)))
-    return fail(cudaErrorInvalidValue);
-  if (!up || a.woven) mu = mw;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = up ? launch_product<true>(a, mx, mw, mu, st) : launch_product<false>(a, mx, mw, mu, st);
+  const cudaError_t e = up ? launch_product<true>(a, st) : launch_product<false>(a, st);
   return e == cudaSuccess ? MOE_OK : fail(e);
 }
