@@ -14,8 +14,10 @@
 // Grouping is a stable counting sort: blocks of rows count their pairs per expert into a table,
 // and a second launch turns the table into positions (rows that fit one block do both in one
 // launch).
+#include <atomic>
 #include <cfloat>
 #include <cmath>
+#include <cstddef>
 
 #include "host.h"
 #include "rows.cuh"
@@ -24,7 +26,7 @@ namespace {
 
 using namespace moe_rows;
 
-constexpr int kRThreads = 512;
+constexpr int kRThreads = 1024;
 constexpr int kRWarps = kRThreads / 32;
 constexpr int kMaxBlocks = 148;   // blocks of rows, and rows of the count table
 constexpr int kMaxE = MOE_ROUTE_MAX_EXPERTS;
@@ -37,6 +39,7 @@ struct RouteArgs {
   int E, k, routing, norm, raw, bias, G, keep, top2;
   int lanes, per;      // lanes of a group, experts of a lane
   int f32;
+  int vec;             // a lane's experts are whole aligned vectors of the row
   float rsf;
   const void* logits;
   const float* bias_p;
@@ -57,10 +60,9 @@ __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-template <typename R>
-__device__ __forceinline__ R score_of(int routing, R l) {
-  if (routing == MOE_ROUTE_SQRTSOFTPLUS) return sqrt(fmax(l, (R)0) + log1p(exp(-fabs(l))));
-  return (R)1 / ((R)1 + exp(-l));
+__device__ __forceinline__ float score_of(int routing, float l) {
+  if (routing == MOE_ROUTE_SQRTSOFTPLUS) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
+  return 1.0f / (1.0f + expf(-l));
 }
 
 template <typename R>
@@ -79,199 +81,342 @@ __device__ __forceinline__ R warp_max(R v) {
 // What a routed row leaves in the warp: lane s < k holds slot s.
 struct Slots {
   int id;           // -1: no expert was left
-  float l;          // its logit
   float top, den;   // softmax: the row's largest logit, and the sum of exp(l - top)
 };
 
-// Routes one row with scores in R. Returns false when a decision hangs on less than R's rounding
-// (R = float only).
-template <int NJ, typename R>
-__device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&lg)[NJ],
-                                          const float (&bs)[NJ], Slots& out) {
-  constexpr bool kF32 = sizeof(R) == 4;
-  constexpr R kNone = -INFINITY;
-  const int lane = threadIdx.x & 31;
-  const int g = lane / a.lanes, sub = lane - g * a.lanes;
-  const int gs = a.E / a.G;
-  const bool limited = a.keep < a.G;
-  const bool soft = a.routing == MOE_ROUTE_SOFTMAX;
-  const bool sums = limited && a.top2;               // group scores are sums of values
-  const bool scored = a.bias || (sums && !a.raw);    // scores enter a decision
-  bool sure = true;
-
-  R top = 0, den = 1;
-  if (soft) {
-    float m = -FLT_MAX;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) m = fmaxf(m, lg[j]);
-    top = warp_max(m);
-    if (scored || !a.norm) {
-      den = 0;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) den += exp((R)lg[j] - top);   // masked: exp(-inf) = 0
-      den = warp_sum(den);
-    }
+// This lane's place: its group and its first expert in it.
+struct Place {
+  int g, sub, size, base;
+  __device__ __forceinline__ explicit Place(const RouteArgs& a) {
+    const int lane = threadIdx.x & 31;
+    g = lane / a.lanes;
+    sub = lane - g * a.lanes;
+    size = a.E / a.G;
+    base = g * size + sub * a.per;
   }
-  // keys, in order; the values that group sums are made of
-  R key[NJ], val[NJ];
-  R mag = 0;
+  __device__ __forceinline__ bool real(const RouteArgs& a, int j) const {
+    return g < a.G && j < a.per && sub * a.per + j < size;
+  }
+};
+
+// The same decisions in float64: for the rows that float32 leaves open.
+template <int NJ>
+__device__ __noinline__ void route_row_f64(const RouteArgs& a, long long r, Slots& out) {
+  constexpr double kNone = -INFINITY;
+  const int lane = threadIdx.x & 31;
+  const Place at_(a);
+  const size_t row = (size_t)r * (size_t)a.ld;
+  const bool limited = a.keep < a.G, soft = a.routing == MOE_ROUTE_SOFTMAX;
+  double l[NJ], key[NJ], val[NJ];
+  double top = -FLT_MAX, den = 0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const bool gone = !(lg[j] > -INFINITY);
-    const R l = lg[j];
-    R s = 0;
-    if (scored && !gone) s = soft ? exp(l - top) / den : score_of<R>(a.routing, l);
-    key[j] = gone ? kNone : a.bias ? s + (R)bs[j] : l;
-    val[j] = gone ? kNone : (a.bias || a.raw) ? key[j] : s;
-    if (!gone) mag = fmax(mag, fabs(s) + fabs((R)bs[j]) + (a.raw ? fabs(l) : (R)0));
+    const bool real = at_.real(a, j);
+    const float v = real ? load_one(a.logits, row + at_.base + j, a.f32) : -INFINITY;
+    const float b = real && a.bias ? a.bias_p[at_.base + j] : 0.f;
+    l[j] = v > -INFINITY && b > -INFINITY ? (double)fminf(v, FLT_MAX) : kNone;
+    val[j] = b;
+    top = fmax(top, l[j]);
   }
-  R tol = 0;
-  if (kF32 && (a.bias || sums)) tol = warp_max(mag) * (R)(soft ? 0x1p-18 : 0x1p-20);
-
+  top = warp_max(top);
+  if (soft) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) den += exp(l[j] - top);   // masked: exp(-inf) = 0
+    den = warp_sum(den);
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool gone = !(l[j] > kNone);
+    double s = 0;
+    if (!gone) {
+      if (soft) s = exp(l[j] - top) / den;
+      else if (a.routing == MOE_ROUTE_SQRTSOFTPLUS) s = sqrt(fmax(l[j], 0.0) + log1p(exp(-fabs(l[j]))));
+      else s = 1.0 / (1.0 + exp(-l[j]));
+    }
+    key[j] = gone ? kNone : a.bias ? s + val[j] : l[j];
+    val[j] = gone ? kNone : (a.bias || a.raw) ? key[j] : s;
+  }
   if (limited) {
-    // score of this lane's group: the two largest of its values (or its largest key)
-    R m1 = kNone, m2 = kNone;
+    double m1 = kNone, m2 = kNone;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const R v = a.top2 ? val[j] : key[j];
+      const double v = a.top2 ? val[j] : key[j];
       m2 = fmax(m2, fmin(m1, v));
       m1 = fmax(m1, v);
     }
     for (int o = 1; o < a.lanes; o <<= 1) {
-      const R o1 = __shfl_down_sync(kFull, m1, o), o2 = __shfl_down_sync(kFull, m2, o);
-      if (sub + o < a.lanes) {
+      const double o1 = __shfl_down_sync(kFull, m1, o), o2 = __shfl_down_sync(kFull, m2, o);
+      if (at_.sub + o < a.lanes) {
         m2 = fmax(fmin(m1, o1), fmax(m2, o2));
         m1 = fmax(m1, o1);
       }
     }
-    R of = a.top2 && m2 > kNone ? m1 + m2 : m1;
-    of = __shfl_sync(kFull, of, min(g, a.G - 1) * a.lanes);
+    double of = a.top2 && m2 > kNone ? m1 + m2 : m1;
+    of = __shfl_sync(kFull, of, min(at_.g, a.G - 1) * a.lanes);
     int rank = 0;
     for (int o = 0; o < a.G; ++o) {
-      const R other = __shfl_sync(kFull, of, o * a.lanes);
-      rank += other > of || (other == of && o < g);
+      const double other = __shfl_sync(kFull, of, o * a.lanes);
+      rank += other > of || (other == of && o < at_.g);
     }
-    const bool kept = g < a.G && rank < a.keep && of > kNone;
-    if (kF32 && (sums || a.bias)) {
-      const R low = -warp_max(kept ? -of : kNone);
-      const R high = warp_max(g < a.G && rank >= a.keep ? of : kNone);
-      if (high > kNone && low - high <= 2 * tol) sure = false;
-    }
-    if (!kept) {
+    if (!(at_.g < a.G && rank < a.keep)) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) key[j] = kNone;
     }
   }
-
-  // the lane's best key, lowest expert first
-  const int base = g * gs + sub * a.per;
-  R best = kNone;
-  int at = 0;
-  float bl = 0.f, bb = 0.f;
-  auto pick = [&]() {
-    best = kNone;
+  out.id = -1;
+  for (int s = 0; s < a.k; ++s) {
+    double best = kNone;
+    int at = 0;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
       if (key[j] > best) {
         best = key[j];
         at = j;
-        bl = lg[j];
-        bb = bs[j];
       }
-  };
-  pick();
-  out.id = -1;
-  out.l = 0.f;
-  out.top = (float)top;
-  out.den = (float)den;
-  R prev = 0;
-  float prev_l = 0.f, prev_b = 0.f;
-  const int rounds = a.k + (kF32 && a.bias ? 1 : 0);   // the first loser too: its gap counts
-  for (int s = 0; s < rounds; ++s) {
-    R win;
-    if constexpr (kF32) {
-      const uint32_t w = __reduce_max_sync(kFull, best > kNone ? ordered(best) : 0u);
-      win = w ? unordered(w) : kNone;
-    } else {
-      win = warp_max(best);
-    }
-    if (!(win > kNone)) break;                         // no expert is left
+    const double win = warp_max(best);
+    if (!(win > kNone)) break;
     const int owner = __ffs(__ballot_sync(kFull, best == win)) - 1;
-    const int id = __shfl_sync(kFull, base + at, owner);
-    const float l = __shfl_sync(kFull, bl, owner);
-    if (kF32 && a.bias) {
-      const float b = __shfl_sync(kFull, bb, owner);
-      // equal logits with equal biases tie in any arithmetic
-      if (s > 0 && prev - win <= tol && (l != prev_l || b != prev_b)) sure = false;
-      prev = win;
-      prev_l = l;
-      prev_b = b;
+    const int id = __shfl_sync(kFull, at_.base + at, owner);
+    if (lane == s) out.id = id;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (lane == owner && j == at) key[j] = kNone;
+  }
+}
+
+// Logits of this lane's experts; masked ones (and places without an expert) are -inf.
+template <int NJ>
+__device__ __forceinline__ void load_row(const RouteArgs& a, const Place& at, long long r,
+                                         const float (&bs)[NJ], float (&lg)[NJ]) {
+  const size_t row = (size_t)r * (size_t)a.ld;
+  bool loaded = false;
+  if constexpr (NJ >= 4) {
+    if (a.vec) {
+      loaded = true;
+      if (at.g >= a.G) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) lg[j] = -INFINITY;
+      } else if (a.f32) {
+        const float4* p = (const float4*)((const float*)a.logits + row + at.base);
+#pragma unroll
+        for (int j = 0; j < NJ; j += 4) {
+          const float4 v = p[j / 4];
+          lg[j] = v.x;
+          lg[j + 1] = v.y;
+          lg[j + 2] = v.z;
+          lg[j + 3] = v.w;
+        }
+      } else {
+        const uint2* p = (const uint2*)((const __nv_bfloat16*)a.logits + row + at.base);
+#pragma unroll
+        for (int j = 0; j < NJ; j += 4) {
+          const uint2 v = p[j / 4];
+          lg[j] = bf16_lo(v.x);
+          lg[j + 1] = bf16_hi(v.x);
+          lg[j + 2] = bf16_lo(v.y);
+          lg[j + 3] = bf16_hi(v.y);
+        }
+      }
     }
-    if (lane == s && s < a.k) {
-      out.id = id;
-      out.l = l;
+  }
+  if (!loaded) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) lg[j] = at.real(a, j) ? load_one(a.logits, row + at.base + j, a.f32) : -INFINITY;
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool live = lg[j] > -INFINITY && bs[j] > -INFINITY;   // NaN compares false
+    lg[j] = live ? fminf(lg[j], FLT_MAX) : -INFINITY;
+  }
+}
+
+// Key and id in order: descending key, then ascending id.
+template <int NJ>
+__device__ __forceinline__ void order(uint32_t (&key)[NJ], int (&id)[NJ], int x, int y) {
+  if (key[y] > key[x] || (key[y] == key[x] && id[y] < id[x])) {
+    const uint32_t k = key[x];
+    key[x] = key[y];
+    key[y] = k;
+    const int i = id[x];
+    id[x] = id[y];
+    id[y] = i;
+  }
+}
+
+// Batcher's odd-even merge sort of the lane's experts (NJ a power of two).
+template <int NJ>
+__device__ __forceinline__ void sort_lane(uint32_t (&key)[NJ], int (&id)[NJ]) {
+#pragma unroll
+  for (int p = 1; p < NJ; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < NJ; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < NJ && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order<NJ>(key, id, i + j, i + j + k);
+}
+
+// Routes one row with float32 scores. Returns false when a decision hangs on their rounding: each key
+// and group score is within `tol` of its value (fast exponential and reciprocal: 4 units of 2^-23 of a
+// score, and the sums' roundings; 16 units of 2^-24 of the largest magnitudes are allowed, 64 for
+// softmax, whose scores carry the denominator's rounding too).
+template <int NJ>
+__device__ __forceinline__ bool route_row(const RouteArgs& a, const Place& at, long long r, const float (&lg)[NJ],
+                                          const float (&bs)[NJ], float most_bias, Slots& out) {
+  const int lane = threadIdx.x & 31;
+  const bool limited = a.keep < a.G, soft = a.routing == MOE_ROUTE_SOFTMAX;
+  const bool sums = limited && a.top2;               // group scores are sums of values
+  const bool scored = a.bias || (sums && !a.raw);    // scores enter a decision
+  bool sure = true;
+
+  out.top = 0.f;
+  out.den = 1.f;
+  float inv = 1.f;
+  if (soft && (scored || !a.norm)) {
+    float m = -FLT_MAX, den = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) m = fmaxf(m, lg[j]);
+    m = unordered(__reduce_max_sync(kFull, ordered(m)));
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) den += __expf(lg[j] - m);   // masked: exp(-inf) = 0
+    out.top = m;
+    out.den = warp_sum(den);
+    inv = __fdividef(1.0f, out.den);
+  }
+  float sc[NJ];        // scores, where they decide something
+  float mag = 1.f;     // their largest magnitude
+  if (scored) {
+    if (soft) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) sc[j] = __expf(lg[j] - out.top) * inv;
+    } else if (a.routing == MOE_ROUTE_SIGMOID) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) sc[j] = __fdividef(1.0f, 1.0f + __expf(-lg[j]));
+    } else {
+      mag = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        sc[j] = lg[j] > -INFINITY ? score_of(MOE_ROUTE_SQRTSOFTPLUS, lg[j]) : 0.f;
+        mag = fmaxf(mag, sc[j]);
+      }
+      mag = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
     }
+  } else if (sums) {
+    mag = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) mag = fmaxf(mag, lg[j] > -INFINITY ? fabsf(lg[j]) : 0.f);
+    mag = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
+  }
+  const float tol = (mag + most_bias) * (soft ? 0x1p-18f : 0x1p-20f);
+  float kf[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) kf[j] = a.bias && lg[j] > -INFINITY ? sc[j] + bs[j] : lg[j];
+
+  bool kept = at.g < a.G;
+  if (limited) {
+    // score of this lane's group: the two largest of its values (or its largest key)
+    float m1 = -INFINITY, m2 = -INFINITY;
+    const bool plain = !a.bias && !a.raw && a.top2;   // values are the scores themselves
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const float v = plain && lg[j] > -INFINITY ? sc[j] : kf[j];
+      m2 = fmaxf(m2, fminf(m1, v));
+      m1 = fmaxf(m1, v);
+    }
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      const float o1 = __shfl_down_sync(kFull, m1, o), o2 = __shfl_down_sync(kFull, m2, o);
+      if (at.sub + o < a.lanes) {
+        m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+        m1 = fmaxf(m1, o1);
+      }
+    }
+    float of = a.top2 && m2 > -INFINITY ? m1 + m2 : m1;
+    of = __shfl_sync(kFull, of, min(at.g, a.G - 1) * a.lanes);
+    int rank = 0;
+    for (int o = 0; o < a.G; ++o) {
+      const float other = __shfl_sync(kFull, of, o * a.lanes);
+      rank += other > of || (other == of && o < at.g);
+    }
+    const bool some = at.g < a.G && of > -INFINITY;
+    kept = some && rank < a.keep;
+    if (sums || a.bias) {
+      const float low = unordered(__reduce_min_sync(kFull, kept ? ordered(of) : ordered(INFINITY)));
+      const uint32_t high = __reduce_max_sync(kFull, some && !kept ? ordered(of) : 0u);
+      if (high && low - unordered(high) <= 2.0f * tol) sure = false;
+    }
+  }
+  uint32_t key[NJ];
+  int id[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    key[j] = kept && kf[j] > -INFINITY ? ordered(kf[j]) : 0u;
+    id[j] = at.base + j;
+  }
+  sort_lane<NJ>(key, id);
+
+  out.id = -1;
+  float prev = 0.f;
+  int prev_id = 0;
+  const int rounds = a.k + (a.bias ? 1 : 0);         // with computed keys the first loser's gap counts too
+#pragma unroll 1
+  for (int s = 0; s < rounds; ++s) {
+    const uint32_t win = __reduce_max_sync(kFull, key[0]);
+    if (win == 0u) break;                            // no expert is left
+    const int owner = __ffs(__ballot_sync(kFull, key[0] == win)) - 1;
+    const int got = __shfl_sync(kFull, id[0], owner);
+    if (a.bias) {
+      const float v = unordered(win);
+      if (s > 0 && prev - v <= tol) {
+        // equal logits with equal biases tie in any arithmetic
+        const size_t row = (size_t)r * (size_t)a.ld;
+        if (load_one(a.logits, row + got, a.f32) != load_one(a.logits, row + prev_id, a.f32) ||
+            a.bias_p[got] != a.bias_p[prev_id])
+          sure = false;
+      }
+      prev = v;
+      prev_id = got;
+    }
+    if (lane == s && s < a.k) out.id = got;
     if (lane == owner) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (j == at) key[j] = kNone;
-      pick();
+      for (int j = 0; j + 1 < NJ; ++j) {
+        key[j] = key[j + 1];
+        id[j] = id[j + 1];
+      }
+      key[NJ - 1] = 0u;
     }
   }
   return sure;
 }
 
-// Logits and biases of this lane's experts; masked ones (and places without an expert) are -inf.
-template <int NJ>
-__device__ __forceinline__ void load_row(const RouteArgs& a, long long r, float (&lg)[NJ],
-                                         float (&bs)[NJ]) {
-  const int lane = threadIdx.x & 31;
-  const int g = lane / a.lanes, sub = lane - g * a.lanes;
-  const int gs = a.E / a.G;
-  const size_t row = (size_t)r * (size_t)a.ld;
+// Sum and maximum over the lanes that hold slots (the first 16).
+__device__ __forceinline__ float slots_sum(float v) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int in_group = sub * a.per + j;
-    const bool real = g < a.G && j < a.per && in_group < gs;
-    const int e = g * gs + in_group;
-    float l = real ? load_one(a.logits, row + e, a.f32) : -INFINITY;
-    const float b = real && a.bias ? a.bias_p[e] : 0.f;
-    if (!(l > -INFINITY) || !(b > -INFINITY)) l = -INFINITY;   // NaN compares false
-    lg[j] = fminf(l, FLT_MAX);
-    bs[j] = b;
-  }
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
 }
 
-// The same row with float64 scores, out of line: it is rare, and its registers stay out of the
-// ordinary path.
-template <int NJ>
-__device__ __noinline__ void route_row_f64(const RouteArgs& a, long long r, Slots& out) {
-  float lg[NJ], bs[NJ];
-  load_row<NJ>(a, r, lg, bs);
-  route_row<NJ, double>(a, lg, bs, out);
-}
-
-// Weight of this lane's slot. Renormalised scores are taken relative to a common factor, so that
-// scores that underflow float32 (logits far below zero) keep their ratios.
-__device__ __forceinline__ float weight_of(const RouteArgs& a, const Slots& s) {
+// Weight of this lane's slot, from its logit. Renormalised scores are taken relative to a common factor, so
+// that scores that underflow float32 (logits far below zero) keep their ratios.
+__device__ __forceinline__ float weight_of(const RouteArgs& a, const Slots& s, float l) {
   const bool live = s.id >= 0;
-  const float most = warp_max(live ? s.l : -FLT_MAX);   // the largest selected logit
+  const float most = unordered(__reduce_max_sync(kFull, ordered(live ? l : -FLT_MAX)));   // the largest selected
   float w;
   if (a.routing == MOE_ROUTE_SOFTMAX) {
-    w = a.norm ? expf(s.l - most) : expf(s.l - s.top) / s.den;
+    w = a.norm ? expf(l - most) : expf(l - s.top) / s.den;
   } else if (!a.norm) {
-    w = score_of<float>(a.routing, s.l);
+    w = score_of(a.routing, l);
   } else if (a.routing == MOE_ROUTE_SIGMOID) {
     // e^l / (1 + e^l), over e^most when every logit is negative
-    w = s.l <= 0.f ? expf(s.l - fminf(most, 0.f)) / (1.0f + expf(s.l))
-                   : 1.0f / (1.0f + expf(-s.l));
+    w = l <= 0.f ? expf(l - fminf(most, 0.f)) / (1.0f + expf(l)) : 1.0f / (1.0f + expf(-l));
   } else {
     // far below zero softplus(l) = e^l (its next term is under 2^-24 of it)
-    w = most < -17.0f ? expf(0.5f * (s.l - most)) : score_of<float>(a.routing, s.l);
+    w = most < -17.0f ? expf(0.5f * (l - most)) : score_of(a.routing, l);
   }
   if (!live) w = 0.f;
   if (a.norm) {
-    const float total = warp_sum(w);
+    const float total = slots_sum(w);
     w = total > 0.f ? w / total : 0.f;
   }
   return w * a.rsf;
@@ -282,12 +427,21 @@ template <int NJ>
 __device__ __forceinline__ void route_block(const RouteArgs& a, long long first, long long last,
                                             int* s_count) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place at(a);
+  float bs[NJ], most_bias = 0.f;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    bs[j] = a.bias && at.real(a, j) ? a.bias_p[at.base + j] : 0.f;
+    if (bs[j] > -INFINITY) most_bias = fmaxf(most_bias, fabsf(bs[j]));
+  }
+  most_bias = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most_bias)));
   for (long long r = first + warp; r < last; r += kRWarps) {
-    float lg[NJ], bs[NJ];
-    load_row<NJ>(a, r, lg, bs);
+    float lg[NJ];
+    load_row<NJ>(a, at, r, bs, lg);
     Slots s;
-    if (!route_row<NJ, float>(a, lg, bs, s)) route_row_f64<NJ>(a, r, s);
-    const float w = weight_of(a, s);
+    if (!route_row<NJ>(a, at, r, lg, bs, most_bias, s)) route_row_f64<NJ>(a, r, s);
+    const float l = s.id >= 0 ? fminf(load_one(a.logits, (size_t)r * (size_t)a.ld + s.id, a.f32), FLT_MAX) : 0.f;
+    const float w = weight_of(a, s, l);
     if (lane < a.k) {
       const size_t p = (size_t)r * a.k + lane;
       a.idx[p] = s.id;
@@ -298,10 +452,10 @@ __device__ __forceinline__ void route_block(const RouteArgs& a, long long first,
 }
 
 struct GroupShared {
-  int start[kMaxE];            // first position of this block's pairs of each expert
-  int warp_count[kRWarps][kMaxE];
+  int start[kMaxE];                  // first position of this block's pairs of each expert
+  int all[kMaxE], before[kMaxE];     // pairs of all blocks, and of the blocks before this one
   int scan[kRWarps];
-  int total;
+  int warp_count[kRWarps * kMaxE];   // [warp][expert] (E experts to a row)
 };
 
 // Positions of the block's pairs. `table` holds every block's counts.
@@ -310,16 +464,25 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
                                             GroupShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = a.E;
-  // expert tid: pairs of the blocks before this one, and of all blocks
-  int before = 0, all = 0;
-  if (tid < E) {
+  // pairs of each expert in the blocks before this one, and in all: several threads to an expert
+  if (tid < E) sh.all[tid] = sh.before[tid] = 0;
+  __syncthreads();
+  {
+    const int parts = max(1, min(kRThreads / E, 16)), part = tid / E, e = tid - part * E;
+    if (part < parts) {
+      int before = 0, all = 0;
 #pragma unroll 8
-    for (int b = 0; b < blocks; ++b) {
-      const int c = table[(size_t)b * E + tid];
-      all += c;
-      before += b < block ? c : 0;
+      for (int b = part; b < blocks; b += parts) {
+        const int c = table[b * E + e];
+        all += c;
+        before += b < block ? c : 0;
+      }
+      atomicAdd(&sh.all[e], all);
+      atomicAdd(&sh.before[e], before);
     }
   }
+  __syncthreads();
+  const int all = tid < E ? sh.all[tid] : 0, before = tid < E ? sh.before[tid] : 0;
   int inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -345,7 +508,7 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
   const long long p0 = first * a.k, p1 = last * a.k;
   const long long run = ((p1 - p0 + kRWarps - 1) / kRWarps + 31) / 32 * 32;
   const long long w0 = p0 + warp * run, w1 = min(p1, w0 + run);
-  int* count = sh.warp_count[warp];
+  int* count = sh.warp_count + warp * E;
   for (int e = lane; e < E; e += 32) count[e] = 0;
   __syncwarp();
   for (long long p = w0 + lane; p - lane < w1; p += 32) {
@@ -356,8 +519,8 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
   if (tid < E) {
     int at = sh.start[tid];
     for (int w = 0; w < kRWarps; ++w) {
-      const int c = sh.warp_count[w][tid];
-      sh.warp_count[w][tid] = at;
+      const int c = sh.warp_count[w * E + tid];
+      sh.warp_count[w * E + tid] = at;
       at += c;
     }
   }
@@ -384,6 +547,7 @@ template <int NJ>
 __global__ void __launch_bounds__(kRThreads) route_rows_kernel(const __grid_constant__ RouteArgs a) {
   __shared__ int s_count[kMaxE];
   release_next();
+  wait_previous();
   const long long first = blockIdx.x * a.rows_per_block;
   const long long last = min(a.rows, first + a.rows_per_block);
   if (a.pairs) {
@@ -399,7 +563,8 @@ __global__ void __launch_bounds__(kRThreads) route_rows_kernel(const __grid_cons
 }
 
 __global__ void __launch_bounds__(kRThreads) group_pairs_kernel(const __grid_constant__ RouteArgs a) {
-  __shared__ GroupShared sh;
+  extern __shared__ int4 raw[];
+  GroupShared& sh = *(GroupShared*)raw;
   wait_previous();
   const long long first = blockIdx.x * a.rows_per_block;
   const long long last = min(a.rows, first + a.rows_per_block);
@@ -408,8 +573,11 @@ __global__ void __launch_bounds__(kRThreads) group_pairs_kernel(const __grid_con
 
 template <int NJ>
 __global__ void __launch_bounds__(kRThreads) route_group_kernel(const __grid_constant__ RouteArgs a) {
-  __shared__ GroupShared sh;
+  extern __shared__ int4 raw[];
+  GroupShared& sh = *(GroupShared*)raw;
   __shared__ int s_count[kMaxE];
+  release_next();
+  wait_previous();
   for (int e = threadIdx.x; e < a.E; e += kRThreads) s_count[e] = 0;
   __syncthreads();
   route_block<NJ>(a, 0, a.rows, s_count);
@@ -417,25 +585,49 @@ __global__ void __launch_bounds__(kRThreads) route_group_kernel(const __grid_con
   group_block(a, 0, a.rows, 0, 1, s_count, sh);
 }
 
-template <int NJ>
-cudaError_t launch_route(const RouteArgs& a, int blocks, cudaStream_t st) {
-  if (a.pairs && blocks == 1) {
-    route_group_kernel<NJ><<<1, kRThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  route_rows_kernel<NJ><<<blocks, kRThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !a.pairs) return e;
+// Shared memory of the grouping: the warps' counts of E experts each.
+size_t group_smem(int E) { return offsetof(GroupShared, warp_count) + sizeof(int) * (size_t)kRWarps * E; }
+
+template <typename... P>
+cudaError_t launch_after(void (*kernel)(P...), int blocks, size_t smem, cudaStream_t st, const RouteArgs& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kRThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, group_pairs_kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// Opts a kernel into the grouping's shared memory, once per device.
+template <auto kernel>
+cudaError_t allow_group_smem() {
+  static std::atomic<bool> done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GroupShared));
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+template <int NJ>
+cudaError_t launch_route(const RouteArgs& a, int blocks, cudaStream_t st) {
+  cudaError_t e;
+  if (a.pairs && blocks == 1) {
+    if ((e = allow_group_smem<route_group_kernel<NJ>>()) != cudaSuccess) return e;
+    return launch_after(route_group_kernel<NJ>, 1, group_smem(a.E), st, a);
+  }
+  if (a.pairs && (e = allow_group_smem<group_pairs_kernel>()) != cudaSuccess) return e;
+  e = launch_after(route_rows_kernel<NJ>, blocks, 0, st, a);
+  if (e != cudaSuccess || !a.pairs) return e;
+  return launch_after(group_pairs_kernel, blocks, group_smem(a.E), st, a);
 }
 
 int check_cfg(const moe_route_cfg* c, int64_t rows) {
@@ -526,6 +718,9 @@ extern "C" int moe_route_rows(const moe_route_cfg* cfg, int64_t rows, const void
   a.lanes = 32 / a.G;
   a.per = (size + a.lanes - 1) / a.lanes;
   a.f32 = c.logits_dtype == MOE_FMT_F32;
+  // whole vectors of four: every lane of a group is full, and rows start on a vector
+  a.vec = a.per >= 4 && (a.per & (a.per - 1)) == 0 && size == a.per * a.lanes && ld_logits % 4 == 0 &&
+          aligned_to(logits, 4 * float_bytes(c.logits_dtype));
   a.rsf = c.routed_scaling_factor;
   a.logits = logits; a.bias_p = expert_bias; a.idx = idx; a.weights = weights;
   a.pairs = group ? sorted_pairs : nullptr;
