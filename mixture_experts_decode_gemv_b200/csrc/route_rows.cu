@@ -48,7 +48,8 @@ struct RouteArgs {
   int* pairs;          // grouping (NULL: none)
   int* offsets;
   int* perm;
-  int* table;          // [blocks][E] pairs per block and expert
+  int* table;          // [blocks][pitch] pairs per block and expert
+  int pitch;           // E, rounded up to a whole int4
 };
 
 // Order-preserving map of a float key to uint32; every key that can be selected maps above 0.
@@ -99,6 +100,36 @@ struct Place {
   }
 };
 
+__device__ __forceinline__ double score64(int routing, double l) {
+  if (routing == MOE_ROUTE_SQRTSOFTPLUS) return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
+  return 1.0 / (1.0 + exp(-l));
+}
+
+// Puts the experts that lanes 0 .. n-1 hold into the order of their float64 keys (score + bias): the rows
+// where float32 has found the experts of the first n places, but not their order.
+__device__ __noinline__ void settle_order(const RouteArgs& a, long long r, int n, Slots& s) {
+  const int lane = threadIdx.x & 31;
+  double key = -INFINITY;
+  const int id = s.id;
+  if (lane < n && id >= 0) {
+    const float l = fminf(load_one(a.logits, (size_t)r * (size_t)a.ld + id, a.f32), FLT_MAX);
+    key = score64(a.routing, (double)l) + (double)a.bias_p[id];
+  }
+  int rank = 0;
+  for (int o = 0; o < n; ++o) {
+    const double other = __shfl_sync(kFull, key, o);
+    const int other_id = __shfl_sync(kFull, id, o);
+    rank += other > key || (other == key && other_id < id);
+  }
+  // lane `rank` takes this lane's expert
+  int got = -1;
+  for (int o = 0; o < n; ++o) {
+    const int at = __shfl_sync(kFull, rank, o), from = __shfl_sync(kFull, id, o);
+    if (lane == at) got = from;
+  }
+  s.id = lane < n ? got : -1;
+}
+
 // The same decisions in float64: for the rows that float32 leaves open.
 template <int NJ>
 __device__ __noinline__ void route_row_f64(const RouteArgs& a, long long r, Slots& out) {
@@ -130,8 +161,7 @@ __device__ __noinline__ void route_row_f64(const RouteArgs& a, long long r, Slot
     double s = 0;
     if (!gone) {
       if (soft) s = exp(l[j] - top) / den;
-      else if (a.routing == MOE_ROUTE_SQRTSOFTPLUS) s = sqrt(fmax(l[j], 0.0) + log1p(exp(-fabs(l[j]))));
-      else s = 1.0 / (1.0 + exp(-l[j]));
+      else s = score64(a.routing, l[j]);
     }
     key[j] = gone ? kNone : a.bias ? s + val[j] : l[j];
     val[j] = gone ? kNone : (a.bias || a.raw) ? key[j] : s;
@@ -190,7 +220,7 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, const Place& at, lo
                                          const float (&bs)[NJ], float (&lg)[NJ]) {
   const size_t row = (size_t)r * (size_t)a.ld;
   bool loaded = false;
-  if constexpr (NJ >= 4) {
+  if constexpr (NJ >= 4 && NJ % 4 == 0) {
     if (a.vec) {
       loaded = true;
       if (at.g >= a.G) {
@@ -230,20 +260,19 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, const Place& at, lo
   }
 }
 
-// Key and id in order: descending key, then ascending id.
+// Key and id in order: descending key, then ascending id. Selects, not branches.
 template <int NJ>
 __device__ __forceinline__ void order(uint32_t (&key)[NJ], int (&id)[NJ], int x, int y) {
-  if (key[y] > key[x] || (key[y] == key[x] && id[y] < id[x])) {
-    const uint32_t k = key[x];
-    key[x] = key[y];
-    key[y] = k;
-    const int i = id[x];
-    id[x] = id[y];
-    id[y] = i;
-  }
+  const uint32_t kx = key[x], ky = key[y];
+  const int ix = id[x], iy = id[y];
+  const bool swap = ky > kx || (ky == kx && iy < ix);
+  key[x] = max(kx, ky);
+  key[y] = min(kx, ky);
+  id[x] = swap ? iy : ix;
+  id[y] = swap ? ix : iy;
 }
 
-// Batcher's odd-even merge sort of the lane's experts (NJ a power of two).
+// Batcher's odd-even merge sort of the lane's experts.
 template <int NJ>
 __device__ __forceinline__ void sort_lane(uint32_t (&key)[NJ], int (&id)[NJ]) {
 #pragma unroll
@@ -257,18 +286,21 @@ __device__ __forceinline__ void sort_lane(uint32_t (&key)[NJ], int (&id)[NJ]) {
           if (i + j + k < NJ && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order<NJ>(key, id, i + j, i + j + k);
 }
 
-// Routes one row with float32 scores. Returns false when a decision hangs on their rounding: each key
+enum Verdict { kSure, kOrderOpen, kOpen };
+
+// Routes one row with float32 scores and tells which decisions hang on their rounding: none, the order of
+// the experts found (k + 1 of them, one to a lane), or more. Each key
 // and group score is within `tol` of its value (fast exponential and reciprocal: 4 units of 2^-23 of a
 // score, and the sums' roundings; 16 units of 2^-24 of the largest magnitudes are allowed, 64 for
 // softmax, whose scores carry the denominator's rounding too).
 template <int NJ>
-__device__ __forceinline__ bool route_row(const RouteArgs& a, const Place& at, long long r, const float (&lg)[NJ],
+__device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at, long long r, const float (&lg)[NJ],
                                           const float (&bs)[NJ], float most_bias, Slots& out) {
   const int lane = threadIdx.x & 31;
   const bool limited = a.keep < a.G, soft = a.routing == MOE_ROUTE_SOFTMAX;
   const bool sums = limited && a.top2;               // group scores are sums of values
   const bool scored = a.bias || (sums && !a.raw);    // scores enter a decision
-  bool sure = true;
+  bool sure = true, ordered_ok = true;
 
   out.top = 0.f;
   out.den = 1.f;
@@ -372,12 +404,12 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const Place& at, l
         const size_t row = (size_t)r * (size_t)a.ld;
         if (load_one(a.logits, row + got, a.f32) != load_one(a.logits, row + prev_id, a.f32) ||
             a.bias_p[got] != a.bias_p[prev_id])
-          sure = false;
+          ordered_ok = false;
       }
       prev = v;
       prev_id = got;
     }
-    if (lane == s && s < a.k) out.id = got;
+    if (lane == s) out.id = got;
     if (lane == owner) {
 #pragma unroll
       for (int j = 0; j + 1 < NJ; ++j) {
@@ -387,7 +419,11 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const Place& at, l
       key[NJ - 1] = 0u;
     }
   }
-  return sure;
+  if (!ordered_ok) {   // the experts found are those of the first k + 1 places if the next is clearly below
+    const uint32_t next = __reduce_max_sync(kFull, key[0]);
+    if (next && prev - unordered(next) <= tol) sure = false;
+  }
+  return !sure ? kOpen : ordered_ok ? kSure : kOrderOpen;
 }
 
 // Sum and maximum over the lanes that hold slots (the first 16).
@@ -439,7 +475,10 @@ __device__ __forceinline__ void route_block(const RouteArgs& a, long long first,
     float lg[NJ];
     load_row<NJ>(a, at, r, bs, lg);
     Slots s;
-    if (!route_row<NJ>(a, at, r, lg, bs, most_bias, s)) route_row_f64<NJ>(a, r, s);
+    const Verdict v = route_row<NJ>(a, at, r, lg, bs, most_bias, s);
+    if (v == kOrderOpen) settle_order(a, r, a.k + 1, s);
+    else if (v == kOpen) route_row_f64<NJ>(a, r, s);
+    if (lane >= a.k) s.id = -1;
     const float l = s.id >= 0 ? fminf(load_one(a.logits, (size_t)r * (size_t)a.ld + s.id, a.f32), FLT_MAX) : 0.f;
     const float w = weight_of(a, s, l);
     if (lane < a.k) {
@@ -453,9 +492,8 @@ __device__ __forceinline__ void route_block(const RouteArgs& a, long long first,
 
 struct GroupShared {
   int start[kMaxE];                  // first position of this block's pairs of each expert
-  int all[kMaxE], before[kMaxE];     // pairs of all blocks, and of the blocks before this one
   int scan[kRWarps];
-  int warp_count[kRWarps * kMaxE];   // [warp][expert] (E experts to a row)
+  alignas(16) int warp_count[kRWarps * kMaxE];   // [warp][expert] (E experts to a row), and sums of the table
 };
 
 // Positions of the block's pairs. `table` holds every block's counts.
@@ -464,25 +502,32 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
                                             GroupShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = a.E;
-  // pairs of each expert in the blocks before this one, and in all: several threads to an expert
-  if (tid < E) sh.all[tid] = sh.before[tid] = 0;
-  __syncthreads();
+  // pairs of each expert in the blocks before this one, and in all; a thread takes four experts of
+  // every parts-th block, with all of its loads on their way at once
+  int before = 0, all = 0;
   {
-    const int parts = max(1, min(kRThreads / E, 16)), part = tid / E, e = tid - part * E;
+    const int quads = a.pitch / 4, parts = min(kRThreads / quads, kRWarps / 2);
+    const int part = tid / quads, q = tid - part * quads;
+    int4* sums = (int4*)sh.warp_count;   // [parts][2][quads]
     if (part < parts) {
-      int before = 0, all = 0;
-#pragma unroll 8
+      int4 n = {0, 0, 0, 0}, m = {0, 0, 0, 0};
+#pragma unroll 10
       for (int b = part; b < blocks; b += parts) {
-        const int c = table[b * E + e];
-        all += c;
-        before += b < block ? c : 0;
+        const int4 c = *(const int4*)(table + b * a.pitch + 4 * q);
+        const bool low = b < block;
+        n.x += c.x; n.y += c.y; n.z += c.z; n.w += c.w;
+        m.x += low ? c.x : 0; m.y += low ? c.y : 0; m.z += low ? c.z : 0; m.w += low ? c.w : 0;
       }
-      atomicAdd(&sh.all[e], all);
-      atomicAdd(&sh.before[e], before);
+      sums[(2 * part) * quads + q] = n;
+      sums[(2 * part + 1) * quads + q] = m;
     }
+    __syncthreads();
+    if (tid < E)
+      for (int r = 0; r < parts; ++r) {
+        all += sh.warp_count[2 * r * a.pitch + tid];
+        before += sh.warp_count[(2 * r + 1) * a.pitch + tid];
+      }
   }
-  __syncthreads();
-  const int all = tid < E ? sh.all[tid] : 0, before = tid < E ? sh.before[tid] : 0;
   int inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -508,17 +553,20 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
   const long long p0 = first * a.k, p1 = last * a.k;
   const long long run = ((p1 - p0 + kRWarps - 1) / kRWarps + 31) / 32 * 32;
   const long long w0 = p0 + warp * run, w1 = min(p1, w0 + run);
+  const int busy = (int)((p1 - p0 + run - 1) / run);   // warps that have pairs
   int* count = sh.warp_count + warp * E;
-  for (int e = lane; e < E; e += 32) count[e] = 0;
-  __syncwarp();
-  for (long long p = w0 + lane; p - lane < w1; p += 32) {
-    const int e = p < w1 ? a.idx[p] : -1;
-    if (e >= 0) atomicAdd(count + e, 1);
+  if (warp < busy) {
+    for (int e = lane; e < E; e += 32) count[e] = 0;
+    __syncwarp();
+    for (long long p = w0 + lane; p - lane < w1; p += 32) {
+      const int e = p < w1 ? a.idx[p] : -1;
+      if (e >= 0) atomicAdd(count + e, 1);
+    }
   }
   __syncthreads();
   if (tid < E) {
     int at = sh.start[tid];
-    for (int w = 0; w < kRWarps; ++w) {
+    for (int w = 0; w < busy; ++w) {
       const int c = sh.warp_count[w * E + tid];
       sh.warp_count[w * E + tid] = at;
       at += c;
@@ -545,20 +593,20 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
 
 template <int NJ>
 __global__ void __launch_bounds__(kRThreads) route_rows_kernel(const __grid_constant__ RouteArgs a) {
-  __shared__ int s_count[kMaxE];
+  __shared__ __align__(16) int s_count[kMaxE];
   release_next();
   wait_previous();
   const long long first = blockIdx.x * a.rows_per_block;
   const long long last = min(a.rows, first + a.rows_per_block);
   if (a.pairs) {
-    for (int e = threadIdx.x; e < a.E; e += kRThreads) s_count[e] = 0;
+    for (int e = threadIdx.x; e < kMaxE; e += kRThreads) s_count[e] = 0;
     __syncthreads();
   }
   route_block<NJ>(a, first, last, s_count);
   if (a.pairs) {
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kRThreads)
-      a.table[(size_t)blockIdx.x * a.E + e] = s_count[e];
+    for (int e = threadIdx.x; e < a.pitch; e += kRThreads)
+      a.table[(size_t)blockIdx.x * a.pitch + e] = s_count[e];
   }
 }
 
@@ -575,18 +623,20 @@ template <int NJ>
 __global__ void __launch_bounds__(kRThreads) route_group_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ int4 raw[];
   GroupShared& sh = *(GroupShared*)raw;
-  __shared__ int s_count[kMaxE];
+  __shared__ __align__(16) int s_count[kMaxE];
   release_next();
   wait_previous();
-  for (int e = threadIdx.x; e < a.E; e += kRThreads) s_count[e] = 0;
+  for (int e = threadIdx.x; e < kMaxE; e += kRThreads) s_count[e] = 0;
   __syncthreads();
   route_block<NJ>(a, 0, a.rows, s_count);
   __syncthreads();   // also orders the block's idx writes before its reads of them
   group_block(a, 0, a.rows, 0, 1, s_count, sh);
 }
 
+int pitch_of(int E) { return (E + 3) / 4 * 4; }
+
 // Shared memory of the grouping: the warps' counts of E experts each.
-size_t group_smem(int E) { return offsetof(GroupShared, warp_count) + sizeof(int) * (size_t)kRWarps * E; }
+size_t group_smem(int E) { return offsetof(GroupShared, warp_count) + sizeof(int) * (size_t)kRWarps * pitch_of(E); }
 
 template <typename... P>
 cudaError_t launch_after(void (*kernel)(P...), int blocks, size_t smem, cudaStream_t st, const RouteArgs& a) {
@@ -660,7 +710,7 @@ long long blocks_of(int64_t rows) {
 }
 
 size_t workspace_of(const moe_route_cfg& c, int64_t rows) {
-  const size_t table = (size_t)blocks_of(rows) * c.num_experts * sizeof(int);
+  const size_t table = (size_t)blocks_of(rows) * pitch_of(c.num_experts) * sizeof(int);
   return (table + 255) / 256 * 256;
 }
 
@@ -725,11 +775,17 @@ extern "C" int moe_route_rows(const moe_route_cfg* cfg, int64_t rows, const void
   a.logits = logits; a.bias_p = expert_bias; a.idx = idx; a.weights = weights;
   a.pairs = group ? sorted_pairs : nullptr;
   a.offsets = expert_offsets; a.perm = token_to_perm; a.table = (int*)workspace;
-  const cudaError_t e = a.per <= 1   ? launch_route<1>(a, blocks, st)
-                        : a.per <= 2 ? launch_route<2>(a, blocks, st)
-                        : a.per <= 4 ? launch_route<4>(a, blocks, st)
-                        : a.per <= 8 ? launch_route<8>(a, blocks, st)
-                        : a.per <= 16 ? launch_route<16>(a, blocks, st)
-                                      : launch_route<32>(a, blocks, st);
+  a.pitch = pitch_of(a.E);
+  cudaError_t e;
+  switch (a.per) {
+    case 1: e = launch_route<1>(a, blocks, st); break;
+    case 2: e = launch_route<2>(a, blocks, st); break;
+    case 3: e = launch_route<3>(a, blocks, st); break;
+    case 4: e = launch_route<4>(a, blocks, st); break;
+    case 5: e = launch_route<5>(a, blocks, st); break;
+    case 6: e = launch_route<6>(a, blocks, st); break;
+    case 7: case 8: e = launch_route<8>(a, blocks, st); break;
+    default: e = a.per <= 16 ? launch_route<16>(a, blocks, st) : launch_route<32>(a, blocks, st);
+  }
   return e == cudaSuccess ? MOE_OK : fail(e);
 }
