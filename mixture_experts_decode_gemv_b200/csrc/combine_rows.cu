@@ -1,8 +1,9 @@
 // moe_combine_rows: out[r] = sum_s weights[r, s] * y[token_to_perm[r * k + s]] + gate[r] * shared[r].
 //
-// Bound by memory: every row of y is read once and every row of out written once. A thread takes
-// one column of a row and adds its slots in slot order in float32, so a row's result does not
-// depend on how the rows are shared out; the one rounding is the store.
+// Bound by memory: every row of y is read once and every row of out written once. A thread takes up to 16
+// bytes of y in a row (one vector, or several narrower ones where the row's length or address allows no
+// whole vector), has the loads of eight slots on their way together, and adds them in slot order in float32:
+// a row's result does not depend on how the rows are shared out, and the one rounding is the store.
 #include "host.h"
 #include "rows.cuh"
 
@@ -13,7 +14,7 @@ using namespace moe_rows;
 struct CombineArgs {
   long long rows, ld_y, y_rows, ld_shared, ld_out;
   int n, top_k;
-  bool y_f32, out_f32;
+  int lanes;           // threads of a row
   const void* y;
   const int* perm;
   const float* weights;
@@ -22,27 +23,120 @@ struct CombineArgs {
   void* out;
 };
 
-constexpr int kCThreads = 128;
+constexpr int kCThreads = 256;
+constexpr int kSlots = 8;    // slots whose loads go together
 
+template <int BYTES>
+struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = uint32_t; };
+template <> struct Raw<2> { using type = uint16_t; };
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_float(float* p, float v) { *p = v; }
+__device__ __forceinline__ void from_float(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// VEC elements of Y to a load, U loads to a thread, `lanes` vectors apart.
+template <typename Y, typename O, int VEC, int U>
 __global__ void __launch_bounds__(kCThreads) combine_rows_kernel(const __grid_constant__ CombineArgs a) {
-  const int col = blockIdx.x * kCThreads + threadIdx.x;
-  if (col >= a.n) return;
-  for (long long r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    float acc = 0.f;
-    for (int s = 0; s < a.top_k; ++s) {
-      const long long at = a.perm[r * a.top_k + s];
-      if (at < 0 || at >= a.y_rows) continue;
-      const float w = a.weights ? a.weights[r * a.top_k + s] : 1.0f;
-      acc = fmaf(w, load_one(a.y, (size_t)at * a.ld_y + col, a.y_f32), acc);
+  using RawY = typename Raw<VEC * sizeof(Y)>::type;
+  union Piece {
+    RawY raw;
+    Y v[VEC];
+    __device__ Piece() {}
+  };
+  release_next();
+  wait_previous();
+  const long long id = (long long)blockIdx.x * kCThreads + threadIdx.x;
+  // a 64-bit quotient only where there are that many threads
+  const long long r = a.rows * a.lanes <= 0x7fffffffLL ? (int)id / a.lanes : id / a.lanes;
+  if (r >= a.rows) return;
+  const int first = (int)(id - r * a.lanes), vectors = a.n / VEC;
+  const Y* y = (const Y*)a.y;
+  float acc[U][VEC] = {};
+  for (int s0 = 0; s0 < a.top_k; s0 += kSlots) {
+    int at[kSlots];
+    float w[kSlots];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      const bool real = s0 + s < a.top_k;
+      at[s] = real ? a.perm[r * a.top_k + s0 + s] : -1;
+      w[s] = real && a.weights ? a.weights[r * a.top_k + s0 + s] : 1.0f;
     }
+    Piece p[kSlots][U];
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = first + u * a.lanes;
+        if (at[s] >= 0 && at[s] < a.y_rows && c < vectors)
+          p[s][u].raw = *(const RawY*)(y + (size_t)at[s] * a.ld_y + (size_t)c * VEC);
+      }
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+      if (at[s] >= 0 && at[s] < a.y_rows)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[u][i] = fmaf(w[s], to_float(p[s][u].v[i]), acc[u][i]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = first + u * a.lanes;
+    if (c >= vectors) continue;
     if (a.shared) {
       const float g = a.gate ? a.gate[r] : 1.0f;
-      acc = fmaf(g, load_one(a.shared, (size_t)r * a.ld_shared + col, a.y_f32), acc);
+      Piece p;
+      p.raw = *(const RawY*)((const Y*)a.shared + (size_t)r * a.ld_shared + (size_t)c * VEC);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[u][i] = fmaf(g, to_float(p.v[i]), acc[u][i]);
     }
-    const size_t o = (size_t)r * a.ld_out + col;
-    if (a.out_f32) ((float*)a.out)[o] = acc;
-    else ((__nv_bfloat16*)a.out)[o] = __float2bfloat16_rn(acc);
+    alignas(16) O o[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) from_float(o + i, acc[u][i]);
+    O* out = (O*)a.out + (size_t)r * a.ld_out + (size_t)c * VEC;
+    constexpr int kStore = VEC * sizeof(O) < 16 ? VEC * sizeof(O) : 16;
+    using RawO = typename Raw<kStore>::type;
+#pragma unroll
+    for (int i = 0; i < (int)(VEC * sizeof(O)) / kStore; ++i) ((RawO*)out)[i] = ((const RawO*)o)[i];
   }
+}
+
+template <typename Y, typename O, int VEC>
+cudaError_t launch_combine(CombineArgs a, cudaStream_t st) {
+  constexpr int U = 16 / (int)(VEC * sizeof(Y));
+  a.lanes = (a.n / VEC + U - 1) / U;
+  const long long blocks = (a.rows * a.lanes + kCThreads - 1) / kCThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;   // more output than any device holds
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kCThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_rows_kernel<Y, O, VEC, U>, a);
+}
+
+template <typename Y, typename O>
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st) {
+  // the widest vectors that every row starts on and ends with
+  auto fits = [&](int vec) {
+    const size_t o = vec * sizeof(O) < 16 ? vec * sizeof(O) : 16;
+    return a.n % vec == 0 && a.ld_y % vec == 0 && a.ld_out % vec == 0 && (!a.shared || a.ld_shared % vec == 0) &&
+           moe_host::aligned_to(a.y, vec * sizeof(Y)) && moe_host::aligned_to(a.shared, vec * sizeof(Y)) &&
+           moe_host::aligned_to(a.out, o);
+  };
+  if constexpr (sizeof(Y) == 2) {
+    if (fits(8)) return launch_combine<Y, O, 8>(a, st);
+  }
+  if (fits(4)) return launch_combine<Y, O, 4>(a, st);
+  if (fits(2)) return launch_combine<Y, O, 2>(a, st);
+  return launch_combine<Y, O, 1>(a, st);
 }
 
 }  // namespace
@@ -71,11 +165,12 @@ extern "C" int moe_combine_rows(int64_t rows, int32_t n, int32_t top_k, int32_t 
   CombineArgs a;
   a.rows = rows; a.ld_y = ld_y; a.y_rows = y_rows; a.ld_shared = ld_shared; a.ld_out = ld_out;
   a.n = n; a.top_k = top_k;
-  a.y_f32 = y_dtype == MOE_FMT_F32; a.out_f32 = out_dtype == MOE_FMT_F32;
   a.y = y; a.perm = token_to_perm; a.weights = weights; a.shared = shared; a.gate = shared_gate;
   a.out = out;
-  const dim3 grid((unsigned)((n + kCThreads - 1) / kCThreads), (unsigned)(rows < 65535 ? rows : 65535));
-  combine_rows_kernel<<<grid, kCThreads, 0, (cudaStream_t)stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool y32 = y_dtype == MOE_FMT_F32, o32 = out_dtype == MOE_FMT_F32;
+  const cudaError_t e = y32 ? (o32 ? launch_combine<float, float>(a, st) : launch_combine<float, __nv_bfloat16>(a, st))
+                            : (o32 ? launch_combine<__nv_bfloat16, float>(a, st)
+                                   : launch_combine<__nv_bfloat16, __nv_bfloat16>(a, st));
   return e == cudaSuccess ? MOE_OK : fail(e);
 }

@@ -7,7 +7,11 @@
 // x and q0 * scale are multiples of half an ulp of the scale, and where the choice is open (r near
 // half a scale) r needs at most 24 bits. Comparing r with scale / 2 corrects q0.
 //
-// Bound by memory: each element is read once and one byte is written.
+// Bound by memory: each element is read once and one byte is written. A row stays in the registers of
+// the threads that read it (32, 128 or 512 of them, eight elements to a load) between the pass for its
+// maximum and the pass that rounds. The ordinary element costs five instructions: the quotient rounded
+// by adding 1.5 * 2^23 in the fma that forms it, the remainder, and its largest magnitude so far; only
+// where that reaches half a scale are the group's eight elements rounded again with care.
 #include "host.h"
 #include "rows.cuh"
 
@@ -16,6 +20,7 @@ namespace {
 using namespace moe_rows;
 
 constexpr int kQThreads = 256;
+constexpr int kQGroups = 8;    // groups of eight elements that a thread holds at most
 
 __device__ __forceinline__ int quantise(float x, float scale, float inv, float half) {
   float q = rintf(x * inv);
@@ -26,15 +31,134 @@ __device__ __forceinline__ int quantise(float x, float scale, float inv, float h
   return (int)fminf(127.0f, fmaxf(-127.0f, q));
 }
 
-// One block per row, two passes over it.
+// Scale of a row from the bits of its largest magnitude (infinity and NaN have the largest).
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+         : top == 0u        ? 1.0f
+                            : fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), 0x1p-126f);
+}
+
+// Eight elements as they lie in memory.
+template <bool F32>
+struct Eight {
+  uint4 a, b;   // bf16: a alone
+  __device__ __forceinline__ void load(const void* p) {
+    a = __ldg((const uint4*)p);
+    if (F32) b = __ldg((const uint4*)p + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (F32) {
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    }
+  }
+  // The larger of `top` and the magnitudes, as float32 bits.
+  __device__ __forceinline__ uint32_t most(uint32_t top) const {
+    if constexpr (F32) {
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, w[i] & 0x7fffffffu);
+      return top;
+    } else {
+      const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu),
+                                  __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+      return max(top, max(m << 16, m & 0xffff0000u));
+    }
+  }
+};
+
+// Codes of eight elements.
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float scale, float inv, float half) {
+  constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
+  float t[8], far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t[i] = fmaf(v[i], inv, kRound);
+    far = fmaxf(far, fabsf(fmaf(kRound - t[i], scale, v[i])));
+  }
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(t[i]);
+  if (far >= half) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = (uint32_t)quantise(v[i], scale, inv, half);
+  }
+  auto pack = [](uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+  };
+  return make_uint2(pack(q[0], q[1], q[2], q[3]), pack(q[4], q[5], q[6], q[7]));
+}
+
+// TPR threads to a row, `groups` groups of eight elements to a row (at most TPR * kQGroups).
+template <bool F32, int TPR>
+__global__ void __launch_bounds__(TPR < kQThreads ? kQThreads : TPR)
+quantize_vectors_kernel(long long rows, int groups, const uint8_t* x, long long ld_bytes, int8_t* codes,
+                        long long ld_codes, float* scales) {
+  constexpr int kThreads = TPR < kQThreads ? kQThreads : TPR;
+  __shared__ uint32_t s_max[kThreads / 32];
+  const int t = threadIdx.x % TPR;
+  const long long row = (long long)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+  const bool live = row < rows;   // threads of a row agree; all of the block reach the barrier
+  release_next();
+  wait_previous();
+  Eight<F32> e[kQGroups];
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kQGroups; ++j) {
+    const int g = t + j * TPR;
+    if (live && g < groups) e[j].load(x + row * ld_bytes + (size_t)g * (F32 ? 32 : 16));
+    else e[j].zero();
+  }
+#pragma unroll
+  for (int j = 0; j < kQGroups; ++j) top = e[j].most(top);
+  top = __reduce_max_sync(kFull, top);
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
+    __syncthreads();
+    const int first = threadIdx.x / TPR * (TPR / 32);
+#pragma unroll
+    for (int w = 0; w < TPR / 32; ++w) top = max(top, s_max[first + w]);
+  }
+  if (!live) return;
+  const float scale = scale_of(top);
+  const bool bad = top >= 0x7f800000u;
+  const float inv = __fdiv_rn(1.0f, scale), half = 0.5f * scale;
+  if (t == 0) scales[row] = scale;
+  int8_t* out = codes + row * ld_codes;
+#pragma unroll
+  for (int j = 0; j < kQGroups; ++j) {
+    const int g = t + j * TPR;
+    if (g < groups) {
+      float v[8];
+      e[j].values(v);
+      const uint2 q = codes_of(v, scale, inv, half);
+      *(uint2*)(out + (size_t)g * 8) = bad ? make_uint2(0, 0) : q;
+    }
+  }
+}
+
+// One block per row, two passes over it, any stride and alignment: for what the kernel above does not take
+// (rows that do not start on whole vectors, or are longer than 32768 elements).
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(int k, bool f32, const void* x,
                                                                   long long ld_x, int8_t* codes,
                                                                   long long ld_codes, float* scales) {
   __shared__ uint32_t s_max[kQThreads / 32];
+  release_next();
+  wait_previous();
   const long long row = blockIdx.x;
   const size_t base = (size_t)row * (size_t)ld_x;
   // magnitudes as integers: the order of their bits is theirs, and infinity and NaN are largest
   uint32_t top = 0;
+#pragma unroll 4
   for (int j = threadIdx.x; j < k; j += kQThreads)
     top = max(top, __float_as_uint(load_one(x, base + j, f32)) & 0x7fffffffu);
   top = __reduce_max_sync(kFull, top);
@@ -43,13 +167,44 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(int k, bool f3
   top = s_max[0];
   for (int w = 1; w < kQThreads / 32; ++w) top = max(top, s_max[w]);
   const bool bad = top >= 0x7f800000u;
-  const float scale = bad ? __uint_as_float(0x7fc00000u)
-                      : top == 0 ? 1.0f : fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), 0x1p-126f);
+  const float scale = scale_of(top);
   const float inv = __fdiv_rn(1.0f, scale), half = 0.5f * scale;
   int8_t* out = codes + (size_t)row * (size_t)ld_codes;
+#pragma unroll 4
   for (int j = threadIdx.x; j < k; j += kQThreads)
     out[j] = bad ? (int8_t)0 : (int8_t)quantise(load_one(x, base + j, f32), scale, inv, half);
   if (threadIdx.x == 0) scales[row] = scale;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned blocks, int threads, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, (P)args...);
+}
+
+template <bool F32, int TPR>
+cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
+                           float* scales, cudaStream_t st) {
+  constexpr int threads = TPR < kQThreads ? kQThreads : TPR, per = threads / TPR;
+  return launch_after(quantize_vectors_kernel<F32, TPR>, (unsigned)((rows + per - 1) / per), threads, st, rows, groups,
+                      x, ld_x * (F32 ? 4 : 2), codes, ld_codes, scales);
+}
+
+// Few threads to a row while they can hold it: fewer partial sums to wait for.
+template <bool F32>
+cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
+                           float* scales, cudaStream_t st) {
+  if (groups <= 32 * kQGroups) return launch_vectors<F32, 32>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  if (groups <= 128 * kQGroups) return launch_vectors<F32, 128>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  return launch_vectors<F32, 512>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
 }
 
 }  // namespace
@@ -67,8 +222,13 @@ extern "C" int moe_quantize_rows_int8(int64_t rows, int32_t k, int32_t x_dtype, 
   int rc;
   if ((rc = supported_device())) return rc;
   Range range("moe_quantize_rows_int8");
-  quantize_rows_kernel<<<(unsigned)rows, kQThreads, 0, (cudaStream_t)stream>>>(
-      k, x_dtype == MOE_FMT_F32, x, ld_x, codes, ld_codes, scales);
-  const cudaError_t e = cudaGetLastError();
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool f32 = x_dtype == MOE_FMT_F32;
+  const bool whole = k % 8 == 0 && k <= 512 * kQGroups * 8 && aligned_to(x, 16) && aligned_to(codes, 8) &&
+                     ld_x * (int64_t)float_bytes(x_dtype) % 16 == 0 && ld_codes % 8 == 0;
+  cudaError_t e;
+  if (!whole) e = launch_after(quantize_rows_kernel, (unsigned)rows, kQThreads, st, k, f32, x, ld_x, codes, ld_codes, scales);
+  else if (f32) e = launch_vectors<true>(rows, k / 8, x, ld_x, codes, ld_codes, scales, st);
+  else e = launch_vectors<false>(rows, k / 8, x, ld_x, codes, ld_codes, scales, st);
   return e == cudaSuccess ? MOE_OK : fail(e);
 }
