@@ -19,7 +19,7 @@ namespace {
 
 using namespace moe_rows;
 
-constexpr int kQThreads = 256;
+constexpr int kQThreads = 128;
 constexpr int kQGroups = 8;    // groups of eight elements that a thread holds at most
 
 __device__ __forceinline__ int quantise(float x, float scale, float inv, float half) {
@@ -38,13 +38,21 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
                             : fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), 0x1p-126f);
 }
 
+// A load of what is read once: kept out of L1, fetched into L2 in whole 256 bytes.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
 // Eight elements as they lie in memory.
 template <bool F32>
 struct Eight {
   uint4 a, b;   // bf16: a alone
   __device__ __forceinline__ void load(const void* p) {
-    a = __ldg((const uint4*)p);
-    if (F32) b = __ldg((const uint4*)p + 1);
+    a = load_once((const uint4*)p);
+    if (F32) b = load_once((const uint4*)p + 1);
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void values(float (&v)[8]) const {
@@ -98,8 +106,8 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float scale, floa
   return make_uint2(pack(q[0], q[1], q[2], q[3]), pack(q[4], q[5], q[6], q[7]));
 }
 
-// TPR threads to a row, `groups` groups of eight elements to a row (at most TPR * kQGroups).
-template <bool F32, int TPR>
+// TPR threads to a row, `groups` groups of eight elements to a row (at most TPR * NG).
+template <bool F32, int TPR, int NG>
 __global__ void __launch_bounds__(TPR < kQThreads ? kQThreads : TPR)
 quantize_vectors_kernel(long long rows, int groups, const uint8_t* x, long long ld_bytes, int8_t* codes,
                         long long ld_codes, float* scales) {
@@ -110,16 +118,16 @@ quantize_vectors_kernel(long long rows, int groups, const uint8_t* x, long long 
   const bool live = row < rows;   // threads of a row agree; all of the block reach the barrier
   release_next();
   wait_previous();
-  Eight<F32> e[kQGroups];
+  Eight<F32> e[NG];
   uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < kQGroups; ++j) {
+  for (int j = 0; j < NG; ++j) {
     const int g = t + j * TPR;
     if (live && g < groups) e[j].load(x + row * ld_bytes + (size_t)g * (F32 ? 32 : 16));
     else e[j].zero();
   }
 #pragma unroll
-  for (int j = 0; j < kQGroups; ++j) top = e[j].most(top);
+  for (int j = 0; j < NG; ++j) top = e[j].most(top);
   top = __reduce_max_sync(kFull, top);
   if constexpr (TPR > 32) {
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
@@ -135,7 +143,7 @@ quantize_vectors_kernel(long long rows, int groups, const uint8_t* x, long long 
   if (t == 0) scales[row] = scale;
   int8_t* out = codes + row * ld_codes;
 #pragma unroll
-  for (int j = 0; j < kQGroups; ++j) {
+  for (int j = 0; j < NG; ++j) {
     const int g = t + j * TPR;
     if (g < groups) {
       float v[8];
@@ -190,19 +198,31 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned blocks, int threads, cud
   return cudaLaunchKernelEx(&cfg, kernel, (P)args...);
 }
 
-template <bool F32, int TPR>
+template <bool F32, int TPR, int NG>
 cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
                            float* scales, cudaStream_t st) {
   constexpr int threads = TPR < kQThreads ? kQThreads : TPR, per = threads / TPR;
-  return launch_after(quantize_vectors_kernel<F32, TPR>, (unsigned)((rows + per - 1) / per), threads, st, rows, groups,
-                      x, ld_x * (F32 ? 4 : 2), codes, ld_codes, scales);
+  return launch_after(quantize_vectors_kernel<F32, TPR, NG>, (unsigned)((rows + per - 1) / per), threads, st, rows,
+                      groups, x, ld_x * (F32 ? 4 : 2), codes, ld_codes, scales);
 }
 
-// Few threads to a row while they can hold it: fewer partial sums to wait for.
+template <bool F32, int TPR>
+cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
+                           float* scales, cudaStream_t st) {
+  const int ng = (groups + TPR - 1) / TPR;
+  if (ng <= 2) return launch_vectors<F32, TPR, 2>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  if (ng <= 3) return launch_vectors<F32, TPR, 3>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  if (ng <= 5) return launch_vectors<F32, TPR, 5>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  return launch_vectors<F32, TPR, kQGroups>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+}
+
+// A warp to a row up to 1024 elements, where more threads would idle (65536 rows of 768: 31.7 us against 69
+// with 128 threads to a row); 128 threads up to 8192 (64 rows of 2048: 1.8 us against 2.8 with a warp; 8192
+// of 2048: 12.0 against 13.8); 512 beyond.
 template <bool F32>
 cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
                            float* scales, cudaStream_t st) {
-  if (groups <= 32 * kQGroups) return launch_vectors<F32, 32>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  if (groups <= 128) return launch_vectors<F32, 32>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
   if (groups <= 128 * kQGroups) return launch_vectors<F32, 128>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
   return launch_vectors<F32, 512>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
 }
