@@ -21,10 +21,11 @@ using namespace moe_rows;
 
 struct MatmulArgs {
   long long x_rows, ld_x, rows, ld_out, w_stride, up_stride, ws_stride, ups_stride;
-  int n, k, experts, top_k, act;
+  int n, k, experts, top_k;
   bool out_f32;
   bool woven;      // one map reads the gate and up rows of a tile, as the tile wants them
   bool up_first;   // ... and finds up below gate in memory
+  bool wide_out;   // rows of out start on 16 bytes and end with whole 16 bytes
   const int8_t* x;
   const float* x_scales;
   const int* offsets;
@@ -85,10 +86,18 @@ __device__ __forceinline__ void store_if(bool on, __nv_bfloat16* p, float y) {
   asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p st.global.b16 [%0], %1; }" ::"l"(p), "h"(h), "r"((uint32_t)on));
 }
 
-// The gated activation with one fast exponential and one fast quotient: 2 + 1.2 |g| units of 2^-23
+__device__ __forceinline__ void put(float* p, float y) { *p = y; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float y) { *p = __float2bfloat16_rn(y); }
+
+// What a call does with its products. A template argument: a choice at run time in the middle of a chunk
+// would keep the rows' exponentials from overlapping.
+enum Act { kPlain, kSwiglu, kGeglu };
+
+// The gated activation; SwiGLU with one fast exponential and one fast quotient: 2 + 1.2 |g| units of 2^-23
 // from the exponent's argument, and 2 from the quotient.
-__device__ __forceinline__ float gated(int act, float g, float u) {
-  if (act == MOE_ACT_GEGLU) return moe::gelu_tanh_mul(g, u);
+template <int ACT>
+__device__ __forceinline__ float gated(float g, float u) {
+  if constexpr (ACT == kGeglu) return moe::gelu_tanh_mul(g, u);
   return __fdividef(g * u, 1.0f + __expf(-g));
 }
 
@@ -159,8 +168,9 @@ struct TileWalk {
 
 // Warp 0 loads weights (and rows that lie together), warp 1 issues MMAs, warp 2 fetches the rows' factors,
 // warp 3 tells the first block which gathered stages have landed, warps 4 to 7 gather scattered rows, warps
-// 8 to 23 write out: four for each 32 channels.
-constexpr int kGatherWarps = 4, kWriteWarps = 16, kFirstGather = 4, kFirstWriter = kFirstGather + kGatherWarps;
+// 8 to 15 write out: two for each 32 channels (sixteen of them are left with 80 registers and spill: 226 us
+// against 261 for 8192 rows x 8 of 128 experts, 2 x 768 channels, k = 2048).
+constexpr int kGatherWarps = 4, kWriteWarps = 8, kFirstGather = 4, kFirstWriter = kFirstGather + kGatherWarps;
 constexpr int kPairThreads = 32 * (kFirstWriter + kWriteWarps);
 constexpr int kRowBox = 64;         // rows of x to a load
 constexpr int kPairStages = 6;
@@ -172,42 +182,96 @@ struct PairShared {
   uint32_t tmem;
   int abort;
   TileList list;
-  float2 cols[2][kPairN];   // factor of a row, and whether it is written
+  alignas(16) float scale[2][kPairN];     // factors of the rows
+  uint32_t valid[2][kPairN / 32];         // and which of them are written
+  alignas(16) uint8_t stage[kWriteWarps][1024];
 };
 constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + sizeof(PairShared);
 
+constexpr int kStageBytes = 1024;   // shared memory of a writing warp
 constexpr int kChunk = 16, kChunkStep = kChunk * kWriteWarps / 4;   // rows of a warp's chunk, and to its next
 
-// One chunk of a finished tile: 16 rows of the warp's 32 channels. `p` points at the thread's channel of
-// the chunk's first row; `up` tells whether the thread's lane holds up (its partner gate, 16 lanes away)
-// or gate.
-template <bool ACT, typename T>
-__device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* p, const int (&v)[kChunk], const float2* cols,
-                                            bool in, bool up, float wg, float wu) {
-  const long long ld = a.ld_out;
+// What a writing thread knows of its tile: its channel (of the warp's 32, or 16 with gate and up), the
+// factors of its channel, whether its lane holds up (its partner gate, 16 lanes away), and its 1 KB of
+// shared memory (the warp's).
+struct Writer {
+  int first_ch, channel;
+  float wg, wu;
+  bool up;
+  uint8_t* stage;
+};
+
+// The values of a chunk: row j's value of the thread's channel (with gate and up: of rows j, j + 1 the one
+// that its half of the warp takes). All factors are fetched before the first value is stored: they could
+// not pass the stores.
+template <int ACT, typename F>
+__device__ __forceinline__ void chunk_values(const MatmulArgs& a, const int (&v)[kChunk], const float* scale,
+                                             const Writer& t, F&& take) {
+  float s[kChunk];
 #pragma unroll
-  for (int j = 0; j < kChunk; j += 2) {
-    const float4 f = *(const float4*)(cols + j);
+  for (int j = 0; j < kChunk; j += 4) {
+    const float4 f = *(const float4*)(scale + j);
+    s[j] = f.x;
+    s[j + 1] = f.y;
+    s[j + 2] = f.z;
+    s[j + 3] = f.w;
+  }
+#pragma unroll
+  for (int j = 0; j < kChunk; j += ACT ? 2 : 1) {
     if constexpr (ACT) {
-      // the lane with gate takes row j, the lane with up takes row j + 1
-      const int got = __shfl_xor_sync(kFull, up ? v[j] : v[j + 1], 16);
-      const float s = up ? f.z : f.x;
-      const float g = (float)(up ? got : v[j]) * s * wg;
-      const float u = (float)(up ? v[j + 1] : got) * s * wu;
-      const float y = gated(a.act, g, u);
-      store_if(in && (up ? f.w : f.y) != 0.f, p + (up ? ld : 0), y);
+      const int got = __shfl_xor_sync(kFull, t.up ? v[j] : v[j + 1], 16);
+      const float f = t.up ? s[j + 1] : s[j];
+      const float g = (float)(t.up ? got : v[j]) * f * t.wg;
+      const float u = (float)(t.up ? v[j + 1] : got) * f * t.wu;
+      take(j, gated<ACT>(g, u));
     } else {
-      store_if(in && f.y != 0.f, p, (float)v[j] * f.x * wg);
-      store_if(in && f.w != 0.f, p + ld, (float)v[j + 1] * f.z * wg);
+      take(j, (float)v[j] * s[j] * t.wg);
     }
-    p += 2 * ld;
+  }
+}
+
+// Writes 16 rows of the warp's channels: rows whose bit is set in `rows`. `out` points at the warp's first
+// channel of the chunk's first row. Where rows of out take whole 16-byte stores, the warp lays its values
+// out by row in shared memory and stores 16 bytes to a lane; elsewhere each thread stores its channel.
+template <int ACT, typename T>
+__device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* out, const int (&v)[kChunk], const float* scale,
+                                            uint32_t rows, const Writer& t) {
+  const long long ld = a.ld_out;
+  const int lane = threadIdx.x & 31;
+  if (a.wide_out) {
+    constexpr int kCh = ACT ? 16 : 32, kRowBytes = kCh * (int)sizeof(T), kLanes = kRowBytes / 16;
+    constexpr int kRows = kStageBytes / kRowBytes < kChunk ? kStageBytes / kRowBytes : kChunk;
+    T* mine = (T*)t.stage + (t.channel - t.first_ch) + (ACT && t.up ? kCh : 0);
+    const int r = lane / kLanes, c = lane % kLanes * (16 / (int)sizeof(T));
+    const bool in = t.first_ch + c < a.n;
+    T* to = out + r * ld + c;
+    auto flush = [&](int r0) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kRows * kLanes; i += 32) {
+        const uint4 w = *(const uint4*)(t.stage + (i + lane) * 16);
+        const int row = r0 + i / kLanes;
+        if (in && (rows >> (row + r) & 1)) *(uint4*)(to + row * ld) = w;
+      }
+      __syncwarp();
+    };
+    chunk_values<ACT>(a, v, scale, t, [&](int j, float y) {
+      put(mine + j % kRows * kCh, y);
+      const int next = j + (ACT ? 2 : 1);
+      if (next % kRows == 0) flush(next - kRows);
+    });
+  } else {
+    const bool in = t.channel < a.n;
+    T* p = out + (t.channel - t.first_ch) + (ACT && t.up ? ld : 0);
+    const uint32_t mine = ACT && t.up ? rows >> 1 : rows;
+    chunk_values<ACT>(a, v, scale, t, [&](int j, float y) { store_if(in && (mine >> j & 1), p + j * ld, y); });
   }
 }
 
 // The warp's chunks of the tile; the next one is on its way from tensor memory while one is written.
-template <bool ACT, typename T>
-__device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t d, const float2* cols, int live,
-                                           int c0, bool in, bool up, float wg, float wu) {
+template <int ACT, typename T>
+__device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t d, const float* scale,
+                                           const uint32_t* valid, int live, int c0, const Writer& t) {
   int v[kChunk], w[kChunk];
   if (c0 >= live) return;
   tmem_load16(d + c0, v);
@@ -215,12 +279,12 @@ __device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t
     const int c1 = c0 + kChunkStep, c2 = c1 + kChunkStep;
     tmem_load_wait();
     if (c1 < live) tmem_load16(d + c1, w);
-    write_chunk<ACT>(a, out + c0 * a.ld_out, v, cols + c0, in, up, wg, wu);
+    write_chunk<ACT>(a, out + c0 * a.ld_out, v, scale + c0, valid[c0 / 32] >> (c0 & 16), t);
     __syncwarp();
     if (c1 < live) {
       tmem_load_wait();
       if (c2 < live) tmem_load16(d + c2, v);
-      write_chunk<ACT>(a, out + c1 * a.ld_out, w, cols + c1, in, up, wg, wu);
+      write_chunk<ACT>(a, out + c1 * a.ld_out, w, scale + c1, valid[c1 / 32] >> (c1 & 16), t);
       __syncwarp();
     }
   }
@@ -229,12 +293,13 @@ __device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t
 // Two blocks share a tile of 256 channels (128 with gate and up) x up to 256 rows: each loads half of
 // both operands and holds the accumulators of its channels (int32, 256 columns of tensor memory, two
 // buffers, so that one tile is written out while the next is multiplied).
-template <bool ACT>
+template <int ACT>
 __global__ void __launch_bounds__(kPairThreads, 1)
 matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_x,
                    const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_up) {
   extern __shared__ uint8_t raw[];
-  uint8_t* base = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  // an offset, not a rounded address: the compiler has to see that everything here is shared memory
+  uint8_t* base = raw + (-smem_addr(raw) & 1023);
   PairShared& sh = *(PairShared*)(base + kPairStages * kPairStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
@@ -365,14 +430,21 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     int i0, live, ch;
     for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
+      float f[kPairN / 32];   // fetched before the wait for their place
+      uint32_t valid[kPairN / 32];
+#pragma unroll
+      for (int j = 0; j < kPairN / 32; ++j) {
+        const int c = lane + 32 * j;
+        int row;
+        f[j] = 0.f;
+        valid[j] = __ballot_sync(kFull, c < live && source_row(a, i0 + c, row, f[j]));
+      }
       ok = bar_wait(smem_addr(&sh.cols_free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
       if (!ok) break;
 #pragma unroll
-      for (int c = lane; c < kPairN; c += 32) {
-        int row;
-        float scale = 0.f;
-        const bool real = c < live && source_row(a, i0 + c, row, scale);
-        sh.cols[b][c] = make_float2(scale, real ? 1.f : 0.f);
+      for (int j = 0; j < kPairN / 32; ++j) {
+        sh.scale[b][lane + 32 * j] = f[j];
+        if (lane == j) sh.valid[b][j] = valid[j];
       }
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&sh.cols_full[b]));
@@ -436,7 +508,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       copies_wait_all();
     }
   } else {
-    // ---- epilogue: this warp's 32 channels of every fourth 16 rows
+    // ---- epilogue: this warp's 32 channels of every second 16 rows
     const int quarter = warp & 3, first_row = ((warp - kFirstWriter) >> 2) * kChunk;
     const bool up = ACT && ((lane & 16) != 0) != a.up_first;
     uint32_t tile = 0;
@@ -444,20 +516,23 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     int i0, live, ch;
     for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
-      const int channel = ACT ? ch * kChPair + (int)rank * kChBlock + quarter * 16 + (lane & 15)
-                              : ch * kChPair + (int)rank * kChBlock + quarter * 32 + lane;
-      const bool in = channel < a.n;
-      const float wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)channel * 4) : 0.f;
-      const float wu = ACT && in
-          ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)channel * 4) : 0.f;
+      Writer t;
+      t.first_ch = ch * kChPair + (int)rank * kChBlock + quarter * (ACT ? 16 : 32);
+      t.channel = t.first_ch + (ACT ? lane & 15 : lane);
+      t.up = up;
+      t.stage = sh.stage[warp - kFirstWriter];
+      const bool in = t.channel < a.n;
+      t.wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
+      t.wu = ACT && in
+          ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)t.channel * 4) : 0.f;
       ok = bar_wait(smem_addr(&sh.cols_full[b]), (tile >> 1) & 1, abort, kWaitLimit) &&
            bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
-      const size_t at = (size_t)i0 * a.ld_out + channel;
-      if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, sh.cols[b], live, first_row, in, up, wg, wu);
-      else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, sh.cols[b], live, first_row, in, up, wg, wu);
+      const size_t at = (size_t)i0 * a.ld_out + t.first_ch;
+      if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, sh.scale[b], sh.valid[b], live, first_row, t);
+      else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, sh.scale[b], sh.valid[b], live, first_row, t);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -497,7 +572,8 @@ struct FewShared {
   uint32_t tmem;
   int abort;
   TileList list;
-  float2 cols[4][kFewN];                            // factors of the rows, a copy for each writing warp
+  alignas(16) float scale[4][kFewN];                // factors of the rows, a copy for each writing warp
+  alignas(16) uint8_t stage[4][kStageBytes];
   int red[(kFewN + kFewMaxCluster - 1) * 128];      // sums of this block's rows from every block
 };
 constexpr size_t kFewSmem = 1024 + (size_t)kFewStages * kFewStage + sizeof(FewShared);
@@ -506,12 +582,13 @@ __device__ __forceinline__ void store_remote(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-template <bool ACT>
+template <int ACT>
 __global__ void __launch_bounds__(kFewThreads, 1)
 matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_up) {
   extern __shared__ uint8_t raw[];
-  uint8_t* base = (uint8_t*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  // an offset, not a rounded address: the compiler has to see that everything here is shared memory
+  uint8_t* base = raw + (-smem_addr(raw) & 1023);
   FewShared& sh = *(FewShared*)(base + kFewStages * kFewStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int split = (int)cluster_size(), rank = (int)cluster_rank();
@@ -661,19 +738,25 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     uint32_t tile = 0;
     for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
-      const int channel = ACT ? ch * kCh + quarter * 16 + (lane & 15) : ch * kCh + lane_ch;
-      const bool in = channel < a.n;
-      const float wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)channel * 4) : 0.f;
-      const float wu = ACT && in
-          ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)channel * 4) : 0.f;
+      Writer t;
+      t.first_ch = ch * kCh + quarter * (ACT ? 16 : 32);
+      t.channel = t.first_ch + (ACT ? lane & 15 : lane);
+      t.up = up;
+      t.stage = sh.stage[quarter];
+      const bool in = t.channel < a.n;
+      t.wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
+      t.wu = ACT && in
+          ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)t.channel * 4) : 0.f;
       // factors of the rows that this block writes: slot q is row rank + q * split
-      float2* cols = sh.cols[quarter];
-      for (int q = lane; q < (slots + 15) / 16 * 16; q += 32) {
-        const int c = rank + q * split;
+      float* scale = sh.scale[quarter];
+      uint32_t valid[kFewN / 32];
+#pragma unroll
+      for (int j = 0; j < kFewN / 32; ++j) {
+        const int q = lane + 32 * j, c = rank + q * split;
         int row;
-        float scale = 0.f;
-        const bool real = c < live && source_row(a, i0 + c, row, scale);
-        cols[q] = make_float2(scale, real ? 1.f : 0.f);
+        float f = 0.f;
+        valid[j] = __ballot_sync(kFull, q < slots && c < live && source_row(a, i0 + c, row, f));
+        scale[q] = f;
       }
       __syncwarp();
       ok = (split == 1 || bar_wait(smem_addr(&sh.red_free), (tile & 1) ^ 1, abort, kWaitLimit)) &&
@@ -686,9 +769,10 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
           int v[16];
           tmem_load16(d + c0, v);
           tmem_load_wait();
-          const size_t at = (size_t)(i0 + c0) * a.ld_out + channel;
-          if (a.out_f32) write_chunk<ACT>(a, (float*)a.out + at, v, cols + c0, in, up, wg, wu);
-          else write_chunk<ACT>(a, (__nv_bfloat16*)a.out + at, v, cols + c0, in, up, wg, wu);
+          const size_t at = (size_t)(i0 + c0) * a.ld_out + t.first_ch;
+          const uint32_t rows = (c0 < 32 ? valid[0] : valid[1]) >> (c0 & 16);
+          if (a.out_f32) write_chunk<ACT>(a, (float*)a.out + at, v, scale + c0, rows, t);
+          else write_chunk<ACT>(a, (__nv_bfloat16*)a.out + at, v, scale + c0, rows, t);
           __syncwarp();
         }
         tc_fence_before();
@@ -727,16 +811,17 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
             if (q + j < slots) sum[j] += sh.red[(src * slots + q + j) * 128 + lane_ch];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = cols[q + j];
+          const float f = scale[min(q + j, kFewN - 1)];
           float y;
           if constexpr (ACT) {
             const int other = __shfl_xor_sync(kFull, sum[j], 16);
-            y = gated(a.act, (float)(up ? other : sum[j]) * f.x * wg, (float)(up ? sum[j] : other) * f.x * wu);
+            y = gated<ACT>((float)(up ? other : sum[j]) * f * t.wg, (float)(up ? sum[j] : other) * f * t.wu);
           } else {
-            y = (float)sum[j] * f.x * wg;
+            y = (float)sum[j] * f * t.wg;
           }
-          const bool on = in && !up && q + j < slots && c + j * split < live && f.y != 0.f;
-          const size_t at = (size_t)(i0 + c + j * split) * a.ld_out + channel;
+          const int slot = q + j;
+          const bool on = in && !up && slot < slots && ((slot < 32 ? valid[0] : valid[1]) >> (slot & 31) & 1);
+          const size_t at = (size_t)(i0 + c + j * split) * a.ld_out + t.channel;
           if (a.out_f32) store_if(on, (float*)a.out + at, y);
           else store_if(on, (__nv_bfloat16*)a.out + at, y);
         }
@@ -863,7 +948,7 @@ struct Maps {
   CUtensorMap x, w, up;
 };
 
-template <bool ACT>
+template <int ACT>
 cudaError_t launch_product(MatmulArgs& a, cudaStream_t st) {
   int dev = 0, pairs = 0, clusters = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -981,7 +1066,7 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.ws_stride = c.num_experts > 1 ? w->scale_stride : 0;
   a.up_stride = up && c.num_experts > 1 ? up->expert_stride : 0;
   a.ups_stride = up && c.num_experts > 1 ? up->scale_stride : 0;
-  a.n = c.n; a.k = c.k; a.experts = c.num_experts; a.top_k = c.top_k; a.act = c.activation;
+  a.n = c.n; a.k = c.k; a.experts = c.num_experts; a.top_k = c.top_k;
   a.out_f32 = c.out_dtype == MOE_FMT_F32;
   a.x = x; a.x_scales = x_scales; a.offsets = expert_offsets; a.pairs = sorted_pairs;
   a.pair_weights = pair_weights;
@@ -989,9 +1074,13 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.up = up ? (const int8_t*)up->packed : nullptr;
   a.ups = up ? (const float*)up->scales : nullptr;
   a.out = out;
+  const int64_t per16 = 16 / (int64_t)float_bytes(c.out_dtype);
+  a.wide_out = aligned_to(out, 16) && ld_out % per16 == 0 && c.n % per16 == 0;
   a.status = (int*)workspace;
   if (!encode_tiled()) return fail(cudaErrorNotSupported);
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = up ? launch_product<true>(a, st) : launch_product<false>(a, st);
+  const cudaError_t e = !up                               ? launch_product<kPlain>(a, st)
+                        : c.activation == MOE_ACT_GEGLU ? launch_product<kGeglu>(a, st)
+                                                        : launch_product<kSwiglu>(a, st);
   return e == cudaSuccess ? MOE_OK : fail(e);
 }
