@@ -469,24 +469,33 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
         }
     }
   } else if (warp < kFirstWriter) {
-    // ---- scattered rows of x: eight threads to a row, 16 bytes each, into the swizzled tile
+    // ---- scattered rows of x: eight threads to a row, 16 bytes each, into the swizzled tile. The next
+    // tile's row numbers are fetched while this one's rows are.
     if (a.pairs) {
       const int gt = tid - 32 * kFirstGather, chunk = gt & 7;
       uint32_t s = 0, parity = 1;
       TileWalk walk(first);
-      int i0, live, ch;
-      for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
-        const int half = (live + 31) / 32 * 16;
+      int i0, live, ch, half = 0, pair[8];
+      auto fetch = [&]() {   // pairs of the walk's tile, -1 for rows that it does not have
+        const bool more = walk.get<32>(a, sh.list, ch_tiles, i0, live, ch);
+        half = more ? (live + 31) / 32 * 16 : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = (gt >> 3) + 16 * j, c = (int)rank * half + r;
+          pair[j] = r < half && c < live ? a.pairs[i0 + c] : -1;
+        }
+      };
+      fetch();
+      while (ok && half > 0) {
+        const int rows = half;
         const int8_t* src[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int r = (gt >> 3) + 16 * j;
-          const long long i = (long long)i0 + (int)rank * half + r;
-          int row = 0;
-          float unused;
-          if (!(r < half && i < a.rows && source_row(a, i, row, unused))) row = 0;
-          src[j] = a.x + (size_t)row * a.ld_x + chunk * 16;
+          const int row = pair[j] / a.top_k;
+          src[j] = a.x + (size_t)(pair[j] >= 0 && row < a.x_rows ? row : 0) * a.ld_x + chunk * 16;
         }
+        walk.t += stride;
+        fetch();
         for (int kb = 0; kb < k_steps; ++kb) {
           ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
           if (!ok) break;
@@ -495,7 +504,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int r = (gt >> 3) + 16 * j;
-            if (16 * j < half)
+            if (16 * j < rows)
               copy16(sb + r * kStep + ((chunk ^ (r & 7)) << 4), in_k ? src[j] + kb * kStep : a.x, in_k);
           }
           copies_arrive(smem_addr(&sh.landed[s]));
