@@ -148,7 +148,7 @@ struct TileWalk {
   __device__ __forceinline__ bool get(const MatmulArgs& a, const TileList& list, int ch_tiles, int& i0,
                                       int& live, int& ch) {
     if (t >= list.tiles[a.experts] * ch_tiles) return false;
-    while (list.tiles[e + 1] * ch_tiles <= t) ++e;
+    while (e + 1 < a.experts && list.tiles[e + 1] * ch_tiles <= t) ++e;
     const int n = list.tiles[e + 1] - list.tiles[e];
     int r = t - list.tiles[e] * ch_tiles;
     const int band = r / (kBand * ch_tiles);

@@ -502,6 +502,13 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
                                             GroupShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = a.E;
+  // each warp has a contiguous run of the block's pairs; the first 32 are fetched now
+  const long long p0 = first * a.k, p1 = last * a.k;
+  const long long run = max(32LL, ((p1 - p0 + kRWarps - 1) / kRWarps + 31) / 32 * 32);
+  const long long w0 = p0 + warp * run, w1 = min(p1, w0 + run);
+  const int busy = (int)((p1 - p0 + run - 1) / run);   // warps that have pairs
+  const int head = w0 + lane < w1 ? a.idx[w0 + lane] : -1;
+  auto expert = [&](long long p) { return p == w0 + lane ? head : p < w1 ? a.idx[p] : -1; };
   // pairs of each expert in the blocks before this one, and in all; a thread takes four experts of
   // every parts-th block, with all of its loads on their way at once
   int before = 0, all = 0;
@@ -523,6 +530,7 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
     }
     __syncthreads();
     if (tid < E)
+#pragma unroll 16
       for (int r = 0; r < parts; ++r) {
         all += sh.warp_count[2 * r * a.pitch + tid];
         before += sh.warp_count[(2 * r + 1) * a.pitch + tid];
@@ -536,11 +544,9 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
   }
   if (lane == 31) sh.scan[warp] = inc;
   __syncthreads();
-  int base = 0, total = 0;
-  for (int w = 0; w < kRWarps; ++w) {
-    if (w < warp) base += sh.scan[w];
-    total += sh.scan[w];
-  }
+  static_assert(kRWarps == 32, "one lane to a warp's sum");
+  const int sum = sh.scan[lane];
+  const int base = __reduce_add_sync(kFull, lane < warp ? sum : 0), total = __reduce_add_sync(kFull, sum);
   const int begin = base + inc - all;
   if (tid < E) {
     sh.start[tid] = begin + before;
@@ -549,17 +555,13 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
       if (tid == E - 1) a.offsets[E] = begin + all;
     }
   }
-  // each warp takes a contiguous run of the block's pairs: count, scan over the warps, place
-  const long long p0 = first * a.k, p1 = last * a.k;
-  const long long run = ((p1 - p0 + kRWarps - 1) / kRWarps + 31) / 32 * 32;
-  const long long w0 = p0 + warp * run, w1 = min(p1, w0 + run);
-  const int busy = (int)((p1 - p0 + run - 1) / run);   // warps that have pairs
+  // count, scan over the warps, place
   int* count = sh.warp_count + warp * E;
   if (warp < busy) {
     for (int e = lane; e < E; e += 32) count[e] = 0;
     __syncwarp();
     for (long long p = w0 + lane; p - lane < w1; p += 32) {
-      const int e = p < w1 ? a.idx[p] : -1;
+      const int e = expert(p);
       if (e >= 0) atomicAdd(count + e, 1);
     }
   }
@@ -574,7 +576,7 @@ __device__ __forceinline__ void group_block(const RouteArgs& a, long long first,
   }
   __syncthreads();
   for (long long p = w0 + lane; p - lane < w1; p += 32) {
-    const int e = p < w1 ? a.idx[p] : -1;
+    const int e = expert(p);
     const unsigned same = __match_any_sync(kFull, e);
     int pos = -1;
     if (e >= 0) {
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(kRThreads) route_rows_kernel(const __grid_cons
   __shared__ __align__(16) int s_count[kMaxE];
   release_next();
   wait_previous();
-  const long long first = blockIdx.x * a.rows_per_block;
+  const long long first = min(a.rows, blockIdx.x * a.rows_per_block);   // the last blocks may have none
   const long long last = min(a.rows, first + a.rows_per_block);
   if (a.pairs) {
     for (int e = threadIdx.x; e < kMaxE; e += kRThreads) s_count[e] = 0;
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kRThreads) group_pairs_kernel(const __grid_con
   extern __shared__ int4 raw[];
   GroupShared& sh = *(GroupShared*)raw;
   wait_previous();
-  const long long first = blockIdx.x * a.rows_per_block;
+  const long long first = min(a.rows, blockIdx.x * a.rows_per_block);   // the last blocks may have none
   const long long last = min(a.rows, first + a.rows_per_block);
   group_block(a, first, last, blockIdx.x, gridDim.x, a.table, sh);
 }
