@@ -23,7 +23,7 @@ struct CombineArgs {
   void* out;
 };
 
-constexpr int kCThreads = 256;
+constexpr int kCThreads = 128;
 constexpr int kSlots = 8;    // slots whose loads go together
 
 template <int BYTES>
@@ -32,6 +32,16 @@ template <> struct Raw<16> { using type = uint4; };
 template <> struct Raw<8> { using type = uint2; };
 template <> struct Raw<4> { using type = uint32_t; };
 template <> struct Raw<2> { using type = uint16_t; };
+
+// Loads of what is read once; whole vectors stay out of L1 and are fetched into L2 in 256 bytes.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ T load_once(const T* p) { return __ldg(p); }
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -72,7 +82,7 @@ __global__ void __launch_bounds__(kCThreads) combine_rows_kernel(const __grid_co
       for (int u = 0; u < U; ++u) {
         const int c = first + u * a.lanes;
         if (at[s] >= 0 && at[s] < a.y_rows && c < vectors)
-          p[s][u].raw = *(const RawY*)(y + (size_t)at[s] * a.ld_y + (size_t)c * VEC);
+          p[s][u].raw = load_once((const RawY*)(y + (size_t)at[s] * a.ld_y + (size_t)c * VEC));
       }
 #pragma unroll
     for (int s = 0; s < kSlots; ++s)
