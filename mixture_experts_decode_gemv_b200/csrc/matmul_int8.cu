@@ -101,6 +101,8 @@ __device__ __forceinline__ float gated(float g, float u) {
   return __fdividef(g * u, 1.0f + __expf(-g));
 }
 
+constexpr int kStageBytes = 1024;   // shared memory of a writing warp: two of these, taken in turn
+
 // The row tiles of all experts, in expert order.
 struct TileList {
   int tiles[MOE_ROUTE_MAX_EXPERTS + 1];   // row tiles before each expert
@@ -184,21 +186,20 @@ struct PairShared {
   TileList list;
   alignas(16) float scale[2][kPairN];     // factors of the rows
   uint32_t valid[2][kPairN / 32];         // and which of them are written
-  alignas(16) uint8_t stage[kWriteWarps][1024];
+  alignas(16) uint8_t stage[kWriteWarps][2 * kStageBytes];
 };
 constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + sizeof(PairShared);
 
-constexpr int kStageBytes = 1024;   // shared memory of a writing warp
 constexpr int kChunk = 16, kChunkStep = kChunk * kWriteWarps / 4;   // rows of a warp's chunk, and to its next
 
 // What a writing thread knows of its tile: its channel (of the warp's 32, or 16 with gate and up), the
-// factors of its channel, whether its lane holds up (its partner gate, 16 lanes away), and its 1 KB of
-// shared memory (the warp's).
+// factors of its channel, whether its lane holds up (its partner gate, 16 lanes away), and the warp's shared
+// memory: the half that the next rows go into.
 struct Writer {
   int first_ch, channel;
   float wg, wu;
   bool up;
-  uint8_t* stage;
+  uint8_t *base, *stage;
 };
 
 // The values of a chunk: row j's value of the thread's channel (with gate and up: of rows j, j + 1 the one
@@ -235,30 +236,31 @@ __device__ __forceinline__ void chunk_values(const MatmulArgs& a, const int (&v)
 // out by row in shared memory and stores 16 bytes to a lane; elsewhere each thread stores its channel.
 template <int ACT, typename T>
 __device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* out, const int (&v)[kChunk], const float* scale,
-                                            uint32_t rows, const Writer& t) {
+                                            uint32_t rows, Writer& t) {
   const long long ld = a.ld_out;
   const int lane = threadIdx.x & 31;
   if (a.wide_out) {
     constexpr int kCh = ACT ? 16 : 32, kRowBytes = kCh * (int)sizeof(T), kLanes = kRowBytes / 16;
     constexpr int kRows = kStageBytes / kRowBytes < kChunk ? kStageBytes / kRowBytes : kChunk;
-    T* mine = (T*)t.stage + (t.channel - t.first_ch) + (ACT && t.up ? kCh : 0);
     const int r = lane / kLanes, c = lane % kLanes * (16 / (int)sizeof(T));
     const bool in = t.first_ch + c < a.n;
     T* to = out + r * ld + c;
-    auto flush = [&](int r0) {
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kRows * kLanes; i += 32) {
-        const uint4 w = *(const uint4*)(t.stage + (i + lane) * 16);
-        const int row = r0 + i / kLanes;
-        if (in && (rows >> (row + r) & 1)) *(uint4*)(to + row * ld) = w;
-      }
-      __syncwarp();
-    };
     chunk_values<ACT>(a, v, scale, t, [&](int j, float y) {
-      put(mine + j % kRows * kCh, y);
+      put((T*)t.stage + (t.channel - t.first_ch) + (ACT && t.up ? kCh : 0) + j % kRows * kCh, y);
       const int next = j + (ACT ? 2 : 1);
-      if (next % kRows == 0) flush(next - kRows);
+      if (next % kRows == 0) {
+        // the other half takes the next rows: who writes there has passed the barrier behind its last reads
+        __syncwarp();
+        uint4 w[kRows * kLanes / 32];
+#pragma unroll
+        for (int i = 0; i < kRows * kLanes / 32; ++i) w[i] = *(const uint4*)(t.stage + (32 * i + lane) * 16);
+#pragma unroll
+        for (int i = 0; i < kRows * kLanes / 32; ++i) {
+          const int row = next - kRows + 32 * i / kLanes;
+          if (in && (rows >> (row + r) & 1)) *(uint4*)(to + row * ld) = w[i];
+        }
+        t.stage = t.base + ((t.stage - t.base) ^ kStageBytes);
+      }
     });
   } else {
     const bool in = t.channel < a.n;
@@ -271,7 +273,7 @@ __device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* out, const i
 // The warp's chunks of the tile; the next one is on its way from tensor memory while one is written.
 template <int ACT, typename T>
 __device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t d, const float* scale,
-                                           const uint32_t* valid, int live, int c0, const Writer& t) {
+                                           const uint32_t* valid, int live, int c0, Writer& t) {
   int v[kChunk], w[kChunk];
   if (c0 >= live) return;
   tmem_load16(d + c0, v);
@@ -529,7 +531,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       t.first_ch = ch * kChPair + (int)rank * kChBlock + quarter * (ACT ? 16 : 32);
       t.channel = t.first_ch + (ACT ? lane & 15 : lane);
       t.up = up;
-      t.stage = sh.stage[warp - kFirstWriter];
+      t.base = t.stage = sh.stage[warp - kFirstWriter];
       const bool in = t.channel < a.n;
       t.wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
       t.wu = ACT && in
@@ -582,7 +584,7 @@ struct FewShared {
   int abort;
   TileList list;
   alignas(16) float scale[4][kFewN];                // factors of the rows, a copy for each writing warp
-  alignas(16) uint8_t stage[4][kStageBytes];
+  alignas(16) uint8_t stage[4][2 * kStageBytes];
   int red[(kFewN + kFewMaxCluster - 1) * 128];      // sums of this block's rows from every block
 };
 constexpr size_t kFewSmem = 1024 + (size_t)kFewStages * kFewStage + sizeof(FewShared);
@@ -751,7 +753,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       t.first_ch = ch * kCh + quarter * (ACT ? 16 : 32);
       t.channel = t.first_ch + (ACT ? lane & 15 : lane);
       t.up = up;
-      t.stage = sh.stage[quarter];
+      t.base = t.stage = sh.stage[quarter];
       const bool in = t.channel < a.n;
       t.wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
       t.wu = ACT && in
