@@ -25,7 +25,6 @@ struct MatmulArgs {
   bool out_f32;
   bool woven;      // one map reads the gate and up rows of a tile, as the tile wants them
   bool up_first;   // ... and finds up below gate in memory
-  bool wide_out;   // rows of out start on 16 bytes and end with whole 16 bytes
   const int8_t* x;
   const float* x_scales;
   const int* offsets;
@@ -100,8 +99,6 @@ __device__ __forceinline__ float gated(float g, float u) {
   if constexpr (ACT == kGeglu) return moe::gelu_tanh_mul(g, u);
   return __fdividef(g * u, 1.0f + __expf(-g));
 }
-
-constexpr int kStageBytes = 1024;   // shared memory of a writing warp: two of these, taken in turn
 
 // The row tiles of all experts, in expert order.
 struct TileList {
@@ -186,20 +183,17 @@ struct PairShared {
   TileList list;
   alignas(16) float scale[2][kPairN];     // factors of the rows
   uint32_t valid[2][kPairN / 32];         // and which of them are written
-  alignas(16) uint8_t stage[kWriteWarps][2 * kStageBytes];
 };
 constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + sizeof(PairShared);
 
 constexpr int kChunk = 16, kChunkStep = kChunk * kWriteWarps / 4;   // rows of a warp's chunk, and to its next
 
-// What a writing thread knows of its tile: its channel (of the warp's 32, or 16 with gate and up), the
-// factors of its channel, whether its lane holds up (its partner gate, 16 lanes away), and the warp's shared
-// memory: the half that the next rows go into.
+// What a writing thread knows of its tile: its channel, the factors of that channel, and whether its lane holds
+// up (its partner gate, 16 lanes away).
 struct Writer {
-  int first_ch, channel;
+  int channel;
   float wg, wu;
-  bool up;
-  uint8_t *base, *stage;
+  bool in, up;     // in: the matrix has this channel
 };
 
 // The values of a chunk: row j's value of the thread's channel (with gate and up: of rows j, j + 1 the one
@@ -231,49 +225,27 @@ __device__ __forceinline__ void chunk_values(const MatmulArgs& a, const int (&v)
   }
 }
 
-// Writes 16 rows of the warp's channels: rows whose bit is set in `rows`. `out` points at the warp's first
-// channel of the chunk's first row. Where rows of out take whole 16-byte stores, the warp lays its values
-// out by row in shared memory and stores 16 bytes to a lane; elsewhere each thread stores its channel.
+// Writes 16 rows of the thread's channel: those whose bit is set in `rows`. `out` points at the channel in the
+// chunk's first row. Whole chunks, which most are, go without a predicate to each store. (Laying the chunk out in
+// shared memory for 16-byte stores took as long: 139 us against 138 for 65536 rows over 128 experts, 2048
+// channels, k = 768; with a predicate everywhere 159.)
 template <int ACT, typename T>
 __device__ __forceinline__ void write_chunk(const MatmulArgs& a, T* out, const int (&v)[kChunk], const float* scale,
-                                            uint32_t rows, Writer& t) {
+                                            uint32_t rows, const Writer& t) {
   const long long ld = a.ld_out;
-  const int lane = threadIdx.x & 31;
-  if (a.wide_out) {
-    constexpr int kCh = ACT ? 16 : 32, kRowBytes = kCh * (int)sizeof(T), kLanes = kRowBytes / 16;
-    constexpr int kRows = kStageBytes / kRowBytes < kChunk ? kStageBytes / kRowBytes : kChunk;
-    const int r = lane / kLanes, c = lane % kLanes * (16 / (int)sizeof(T));
-    const bool in = t.first_ch + c < a.n;
-    T* to = out + r * ld + c;
-    chunk_values<ACT>(a, v, scale, t, [&](int j, float y) {
-      put((T*)t.stage + (t.channel - t.first_ch) + (ACT && t.up ? kCh : 0) + j % kRows * kCh, y);
-      const int next = j + (ACT ? 2 : 1);
-      if (next % kRows == 0) {
-        // the other half takes the next rows: who writes there has passed the barrier behind its last reads
-        __syncwarp();
-        uint4 w[kRows * kLanes / 32];
-#pragma unroll
-        for (int i = 0; i < kRows * kLanes / 32; ++i) w[i] = *(const uint4*)(t.stage + (32 * i + lane) * 16);
-#pragma unroll
-        for (int i = 0; i < kRows * kLanes / 32; ++i) {
-          const int row = next - kRows + 32 * i / kLanes;
-          if (in && (rows >> (row + r) & 1)) *(uint4*)(to + row * ld) = w[i];
-        }
-        t.stage = t.base + ((t.stage - t.base) ^ kStageBytes);
-      }
-    });
+  T* p = out + (ACT && t.up ? ld : 0);
+  if (__all_sync(kFull, t.in) && (rows & 0xffffu) == 0xffffu) {
+    chunk_values<ACT>(a, v, scale, t, [&](int j, float y) { put(p + j * ld, y); });
   } else {
-    const bool in = t.channel < a.n;
-    T* p = out + (t.channel - t.first_ch) + (ACT && t.up ? ld : 0);
     const uint32_t mine = ACT && t.up ? rows >> 1 : rows;
-    chunk_values<ACT>(a, v, scale, t, [&](int j, float y) { store_if(in && (mine >> j & 1), p + j * ld, y); });
+    chunk_values<ACT>(a, v, scale, t, [&](int j, float y) { store_if(t.in && (mine >> j & 1), p + j * ld, y); });
   }
 }
 
 // The warp's chunks of the tile; the next one is on its way from tensor memory while one is written.
 template <int ACT, typename T>
 __device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t d, const float* scale,
-                                           const uint32_t* valid, int live, int c0, Writer& t) {
+                                           const uint32_t* valid, int live, int c0, const Writer& t) {
   int v[kChunk], w[kChunk];
   if (c0 >= live) return;
   tmem_load16(d + c0, v);
@@ -528,20 +500,18 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
       Writer t;
-      t.first_ch = ch * kChPair + (int)rank * kChBlock + quarter * (ACT ? 16 : 32);
-      t.channel = t.first_ch + (ACT ? lane & 15 : lane);
+      t.channel = ch * kChPair + (int)rank * kChBlock + quarter * (ACT ? 16 : 32) + (ACT ? lane & 15 : lane);
       t.up = up;
-      t.base = t.stage = sh.stage[warp - kFirstWriter];
-      const bool in = t.channel < a.n;
-      t.wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
-      t.wu = ACT && in
+      t.in = t.channel < a.n;
+      t.wg = t.in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
+      t.wu = ACT && t.in
           ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)t.channel * 4) : 0.f;
       ok = bar_wait(smem_addr(&sh.cols_full[b]), (tile >> 1) & 1, abort, kWaitLimit) &&
            bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
-      const size_t at = (size_t)i0 * a.ld_out + t.first_ch;
+      const size_t at = (size_t)i0 * a.ld_out + t.channel;
       if (a.out_f32) write_tile<ACT>(a, (float*)a.out + at, d, sh.scale[b], sh.valid[b], live, first_row, t);
       else write_tile<ACT>(a, (__nv_bfloat16*)a.out + at, d, sh.scale[b], sh.valid[b], live, first_row, t);
       tc_fence_before();
@@ -584,7 +554,6 @@ struct FewShared {
   int abort;
   TileList list;
   alignas(16) float scale[4][kFewN];                // factors of the rows, a copy for each writing warp
-  alignas(16) uint8_t stage[4][2 * kStageBytes];
   int red[(kFewN + kFewMaxCluster - 1) * 128];      // sums of this block's rows from every block
 };
 constexpr size_t kFewSmem = 1024 + (size_t)kFewStages * kFewStage + sizeof(FewShared);
@@ -750,13 +719,11 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
       Writer t;
-      t.first_ch = ch * kCh + quarter * (ACT ? 16 : 32);
-      t.channel = t.first_ch + (ACT ? lane & 15 : lane);
+      t.channel = ch * kCh + quarter * (ACT ? 16 : 32) + (ACT ? lane & 15 : lane);
       t.up = up;
-      t.base = t.stage = sh.stage[quarter];
-      const bool in = t.channel < a.n;
-      t.wg = in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
-      t.wu = ACT && in
+      t.in = t.channel < a.n;
+      t.wg = t.in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
+      t.wu = ACT && t.in
           ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)t.channel * 4) : 0.f;
       // factors of the rows that this block writes: slot q is row rank + q * split
       float* scale = sh.scale[quarter];
@@ -780,7 +747,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
           int v[16];
           tmem_load16(d + c0, v);
           tmem_load_wait();
-          const size_t at = (size_t)(i0 + c0) * a.ld_out + t.first_ch;
+          const size_t at = (size_t)(i0 + c0) * a.ld_out + t.channel;
           const uint32_t rows = (c0 < 32 ? valid[0] : valid[1]) >> (c0 & 16);
           if (a.out_f32) write_chunk<ACT>(a, (float*)a.out + at, v, scale + c0, rows, t);
           else write_chunk<ACT>(a, (__nv_bfloat16*)a.out + at, v, scale + c0, rows, t);
@@ -831,7 +798,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
             y = (float)sum[j] * f * t.wg;
           }
           const int slot = q + j;
-          const bool on = in && !up && slot < slots && ((slot < 32 ? valid[0] : valid[1]) >> (slot & 31) & 1);
+          const bool on = t.in && !up && slot < slots && ((slot < 32 ? valid[0] : valid[1]) >> (slot & 31) & 1);
           const size_t at = (size_t)(i0 + c + j * split) * a.ld_out + t.channel;
           if (a.out_f32) store_if(on, (float*)a.out + at, y);
           else store_if(on, (__nv_bfloat16*)a.out + at, y);
@@ -1085,8 +1052,6 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.up = up ? (const int8_t*)up->packed : nullptr;
   a.ups = up ? (const float*)up->scales : nullptr;
   a.out = out;
-  const int64_t per16 = 16 / (int64_t)float_bytes(c.out_dtype);
-  a.wide_out = aligned_to(out, 16) && ld_out % per16 == 0 && c.n % per16 == 0;
   a.status = (int*)workspace;
   if (!encode_tiled()) return fail(cudaErrorNotSupported);
   cudaStream_t st = (cudaStream_t)stream;
