@@ -192,7 +192,8 @@ int moe_decode_launches(const moe_cfg* cfg, int m, const moe_expert_table* route
 
 /* Test aid for failure detection without a GPU fault. After this call the persistent kernels'
  * device-side waits (the grid barrier; in the tensor-core kernel also each down job's wait for
- * its expert's gate/up jobs) expect `extra_arrivals` (0 or 1) more arrivals than any launch makes
+ * its expert's gate/up jobs; in moe_matmul_int8 the wait for a stage's operands) expect
+ * `extra_arrivals` (0 or 1) more arrivals than any launch makes
  * and give up after `spin_limit_cycles` SM clock cycles (0: the default budget of about a second).
  * Every wait stays bounded, so each launch ends; its workspace status then reads
  * MOE_ERR_DEVICE_TIMEOUT and its outputs are undefined (call moe_workspace_init before reusing
@@ -323,7 +324,7 @@ int moe_route_workspace_bytes(const moe_route_cfg* cfg, int64_t rows, size_t* ou
  *  weights  [rows, k] s, divided by the sum of the row's k scores when norm_topk_prob, times
  *           routed_scaling_factor
  * Keys and group scores are compared as in 64-bit arithmetic: 32-bit ones decide only where
- * their rounding cannot.
+ * their rounding cannot change the outcome.
  * An expert whose logit or key is -infinity or NaN is masked: it is never selected and has no
  * part in softmax; +infinity counts as the largest finite logit. A slot that finds no expert gets
  * idx -1 and weight 0 (a fully masked row: all its slots). Under norm_topk_prob the weights of
@@ -346,8 +347,8 @@ int moe_route_rows(const moe_route_cfg* cfg, int64_t rows, const void* logits, i
  *  scale = max(max|x| / 127, 2^-126) in float32 (1 for an all-zero row)
  *  q     = x / scale rounded to the nearest integer, ties to even, within -127..127
  * The rounding is that of the exact quotient. A row that holds a NaN or an infinity gets scale
- * NaN and codes 0, so that what is computed from it is NaN. Any k >= 1 and any strides; rows that
- * start on 16 bytes (codes: 8) are read and written in whole vectors. */
+ * NaN and codes 0, so that what is computed from it is NaN. Any k >= 1 and any strides; where k is a
+ * multiple of 8 (up to 32768) and every row starts on 16 bytes (of codes: 8), a row is read once. */
 int moe_quantize_rows_int8(int64_t rows, int32_t k, int32_t x_dtype, const void* x, int64_t ld_x,
                            int8_t* codes, int64_t ld_codes, float* scales, void* stream);
 

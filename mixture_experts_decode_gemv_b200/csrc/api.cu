@@ -604,6 +604,10 @@ namespace moe_host {
 int fail(int cuda_error) { return cuda_fail((cudaError_t)cuda_error); }
 int supported_device() { return check_device(); }
 int sms() { return sm_count(); }
+void test_waits(int* extra_arrivals, long long* limit) {
+  *extra_arrivals = g_test_bar_extra.load();
+  *limit = g_test_spin_limit.load() > 0 ? g_test_spin_limit.load() : kSpinLimit;
+}
 }  // namespace moe_host
 
 extern "C" int moe_workspace_bytes(const moe_cfg* cfg, int m, size_t* out_bytes) {

@@ -17,6 +17,10 @@ int supported_device();
 // Multiprocessors of the current device (cached); 0 when it cannot be asked.
 int sms();
 
+// Settings of moe_debug_barrier_test: arrivals that device-side waits expect beyond those that come, and
+// the cycles after which they give up.
+void test_waits(int* extra_arrivals, long long* limit);
+
 inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 inline bool float_format(int f) { return f == MOE_FMT_F32 || f == MOE_FMT_BF16; }
 inline size_t float_bytes(int f) { return f == MOE_FMT_F32 ? 4 : 2; }

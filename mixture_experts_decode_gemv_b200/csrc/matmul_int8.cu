@@ -36,6 +36,8 @@ struct MatmulArgs {
   const float* ups;
   void* out;
   int* status;
+  int extra;         // arrivals that no one makes (failure-detection tests)
+  long long limit;   // cycles after which a wait gives up
 };
 
 // ---- tiles ---------------------------------------------------------------------------------------
@@ -46,7 +48,7 @@ struct MatmulArgs {
 // and up of a channel meet in one warp of the epilogue, 16 lanes apart.
 
 constexpr int kStep = 128;                    // bytes of k per stage: one swizzle atom wide
-constexpr long long kWaitLimit = 2000000000LL;  // about a second of SM clock cycles
+constexpr long long kSettle = 1000000;        // cycles in which copies and MMAs under way end
 
 // Rows [begin, end) of expert e, within the output whatever the offsets hold.
 __device__ __forceinline__ void expert_range(const MatmulArgs& a, int e, long long& begin,
@@ -162,6 +164,15 @@ struct TileWalk {
     return true;
   }
 };
+
+// After a wait that ran out: time for this block's copies and MMAs under way to end, before its shared and
+// tensor memory go to someone else.
+__device__ __noinline__ void settle() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < kSettle) {
+  }
+  __syncwarp();
+}
 
 // ---- many rows: pairs of blocks ------------------------------------------------------------------
 
@@ -284,7 +295,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
   if (tid == 0) {
     for (int s = 0; s < kPairStages; ++s) {
       // the weights' (and rows') bytes, and gathered rows of both blocks
-      bar_init(smem_addr(&sh.full[s]), a.pairs ? 1 + 2 : 1);
+      bar_init(smem_addr(&sh.full[s]), (a.pairs ? 1 + 2 : 1) + a.extra);
       bar_init(smem_addr(&sh.landed[s]), 32 * kGatherWarps);
       bar_init(smem_addr(&sh.empty[s]), 1);
     }
@@ -327,7 +338,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       const uint32_t bytes = 2 * (kPairA + boxes * kRowBox * kStep);
       const int ch0 = ch * kChPair + (int)rank * kChBlock;
       for (int kb = 0; kb < k_steps; ++kb) {
-        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, a.limit);
         if (!ok) break;
         const uint32_t full = of_rank(smem_addr(&sh.full[s]), 0);
         const uint32_t sa = smem_addr(base + s * kPairStage), sb = sa + kPairA;
@@ -354,7 +365,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     }
     // every stage has been read before the block may end
     for (int j = 0; ok && j < kPairStages; ++j) {
-      ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+      ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, a.limit);
       if (++s == kPairStages) {
         s = 0;
         parity ^= 1;
@@ -371,13 +382,13 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       int i0, live, ch;
       for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
         const uint32_t b = tile & 1;
-        ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
+        ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, abort, a.limit);
         if (!ok) break;
         tc_fence_after();
         const uint32_t desc = i8_desc(256, (live + 31) / 32 * 32);
         const uint32_t d = tmem + b * kPairN;
         for (int kb = 0; kb < k_steps; ++kb) {
-          ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, kWaitLimit);
+          ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, a.limit);
           if (!ok) break;
           tc_fence_after();
           if (elect()) {
@@ -413,7 +424,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
         f[j] = 0.f;
         valid[j] = __ballot_sync(kFull, c < live && source_row(a, i0 + c, row, f[j]));
       }
-      ok = bar_wait(smem_addr(&sh.cols_free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
+      ok = bar_wait(smem_addr(&sh.cols_free[b]), ((tile >> 1) & 1) ^ 1, abort, a.limit);
       if (!ok) break;
 #pragma unroll
       for (int j = 0; j < kPairN / 32; ++j) {
@@ -431,7 +442,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       int i0, live, ch;
       for (; ok && walk.get<32>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride)
         for (int kb = 0; kb < k_steps; ++kb) {
-          ok = bar_wait(smem_addr(&sh.landed[s]), parity, abort, kWaitLimit);
+          ok = bar_wait(smem_addr(&sh.landed[s]), parity, abort, a.limit);
           if (!ok) break;
           fence_async_proxy();
           if (elect()) bar_arrive_cluster(of_rank(smem_addr(&sh.full[s]), 0));
@@ -471,7 +482,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
         walk.t += stride;
         fetch();
         for (int kb = 0; kb < k_steps; ++kb) {
-          ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+          ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, a.limit);
           if (!ok) break;
           const uint32_t sb = smem_addr(base + s * kPairStage) + kPairA;
           const bool in_k = kb * kStep + chunk * 16 < a.k;
@@ -506,8 +517,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
       t.wg = t.in ? *(const float*)((const char*)a.ws + (size_t)walk.e * a.ws_stride + (size_t)t.channel * 4) : 0.f;
       t.wu = ACT && t.in
           ? *(const float*)((const char*)a.ups + (size_t)walk.e * a.ups_stride + (size_t)t.channel * 4) : 0.f;
-      ok = bar_wait(smem_addr(&sh.cols_full[b]), (tile >> 1) & 1, abort, kWaitLimit) &&
-           bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
+      ok = bar_wait(smem_addr(&sh.cols_full[b]), (tile >> 1) & 1, abort, a.limit) &&
+           bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, a.limit);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * kPairN + ((uint32_t)(quarter * 32) << 16);
@@ -529,6 +540,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (*abort) settle();
   cluster_sync();
   if (warp == 1) tmem_free<2>(tmem, 512);
 }
@@ -579,7 +591,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
 
   if (tid == 0) {
     for (int s = 0; s < kFewStages; ++s) {
-      bar_init(smem_addr(&sh.full[s]), 1 + 64);     // the weights' bytes, the threads that copy rows
+      bar_init(smem_addr(&sh.full[s]), 1 + 64 + a.extra);     // the weights' bytes, the threads that copy rows
       bar_init(smem_addr(&sh.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -615,7 +627,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride) {
       const int ch0 = ch * kCh;
       for (int kb = 0; kb < k_steps; ++kb) {
-        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, a.limit);
         if (!ok) break;
         const uint32_t full = smem_addr(&sh.full[s]), sa = smem_addr(base + s * kFewStage);
         const int x = (k_first + kb) * kStep;
@@ -639,7 +651,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     }
     // every stage has been read before the block may end
     for (int j = 0; ok && j < kFewStages; ++j) {
-      ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+      ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, a.limit);
       if (++s == kFewStages) {
         s = 0;
         parity ^= 1;
@@ -650,13 +662,13 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     const uint64_t desc0 = operand_desc(smem_addr(base));
     for (; ok && walk.get<16>(a, sh.list, ch_tiles, i0, live, ch); walk.t += stride, ++tile) {
       const uint32_t b = tile & 1;
-      ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, abort, kWaitLimit);
+      ok = bar_wait(smem_addr(&sh.free[b]), ((tile >> 1) & 1) ^ 1, abort, a.limit);
       if (!ok) break;
       tc_fence_after();
       const uint32_t desc = i8_desc(128, (live + 15) & ~15);
       const uint32_t d = tmem + b * kFewN;
       for (int kb = 0; kb < k_steps; ++kb) {
-        ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, kWaitLimit);
+        ok = bar_wait(smem_addr(&sh.full[s]), parity, abort, a.limit);
         if (!ok) break;
         fence_async_proxy();
         tc_fence_after();
@@ -692,7 +704,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
         src[j] = a.x + (size_t)row * a.ld_x + chunk * 16;
       }
       for (int kb = 0; kb < k_steps; ++kb) {
-        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, kWaitLimit);
+        ok = bar_wait(smem_addr(&sh.empty[s]), parity, abort, a.limit);
         if (!ok) break;
         const uint32_t sb = smem_addr(base + s * kFewStage) + kFewA;
         const int at = (k_first + kb) * kStep;
@@ -737,8 +749,8 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
         scale[q] = f;
       }
       __syncwarp();
-      ok = (split == 1 || bar_wait(smem_addr(&sh.red_free), (tile & 1) ^ 1, abort, kWaitLimit)) &&
-           bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, kWaitLimit);
+      ok = (split == 1 || bar_wait(smem_addr(&sh.red_free), (tile & 1) ^ 1, abort, a.limit)) &&
+           bar_wait(smem_addr(&sh.done[b]), (tile >> 1) & 1, abort, a.limit);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * kFewN + ((uint32_t)(quarter * 32) << 16);
@@ -778,7 +790,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&sh.free[b]));
       if (lane < split) bar_arrive_release(of_rank(smem_addr(&sh.red_full), lane));
-      ok = bar_wait(smem_addr(&sh.red_full), tile & 1, abort, kWaitLimit);
+      ok = bar_wait(smem_addr(&sh.red_full), tile & 1, abort, a.limit);
       if (!ok) break;
       // four rows at a time, so that their loads and exponentials overlap
       for (int q = 0, c = rank; c < live; q += 4, c += 4 * split) {
@@ -815,6 +827,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (*abort) settle();
   cluster_sync();
   if (warp == 1) tmem_free<1>(tmem, 2 * kFewN);
 }
@@ -1053,6 +1066,7 @@ extern "C" int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const 
   a.ups = up ? (const float*)up->scales : nullptr;
   a.out = out;
   a.status = (int*)workspace;
+  test_waits(&a.extra, &a.limit);
   if (!encode_tiled()) return fail(cudaErrorNotSupported);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = !up                               ? launch_product<kPlain>(a, st)

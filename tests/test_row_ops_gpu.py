@@ -496,6 +496,39 @@ def test_product_nan_scale_gives_nan_rows():
     assert np.isnan(got[3]).all() and np.isfinite(np.delete(got, 3, axis=0)).all()
 
 
+@pytest.mark.parametrize("sizes", [[30, 0, 41], [200, 150, 90]])      # single blocks, pairs of blocks
+@pytest.mark.parametrize("layout", ["up first", "one matrix twice", "other strides"])
+def test_product_gate_and_up_wherever_they_lie(layout, sizes):
+    p = Product(11, sum(sizes), 96, 208, sizes=sizes, act="swiglu", out_dtype=F32)
+    E, size = len(sizes), 96 * 208
+    if layout == "up first":                          # one allocation, up below gate
+        both = torch.cat([p.dw[1].view(-1), p.dw[0].view(-1)])
+        p.dw = [both[E * size:].view(E, size), both[: E * size].view(E, size)]
+    elif layout == "one matrix twice":
+        p.w[1], p.dw[1] = p.w[0], p.dw[0]
+    else:
+        wide = torch.full((E, size + 160), 5, dtype=torch.int8, device="cuda")
+        wide[:, :size] = p.dw[1]
+        p.dw[1] = wide
+    p.mats = [int8_matrix(w, s) for w, s in zip(p.dw, p.dws)]
+    p.check(p.run())
+
+
+@pytest.mark.parametrize("rows,gather", [(20, False), (300, False), (300, True)])
+def test_product_wait_that_runs_out(rows, gather):
+    """A stage whose operands never all arrive: the call ends, and the workspace says so."""
+    p = Product(12, rows, 128, 1024, sizes=[rows], top_k=2 if gather else 1, gather=gather)
+    ws, out = workspace(p.ws_bytes), p.new_out()
+    try:
+        B.moe_debug_barrier_test(1, 2_000_000)
+        p.call(out, ws)
+        torch.cuda.synchronize()
+        assert status(ws) == B.MOE_ERR_DEVICE_TIMEOUT
+    finally:
+        B.moe_debug_barrier_test(0, 0)
+    p.check(p.run())
+
+
 def test_product_rows_do_not_depend_on_their_neighbours():
     """A row's bits are the same alone and within any batch."""
     p = Product(6, 300, 160, 528, out_dtype=F32)
