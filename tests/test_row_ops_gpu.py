@@ -1,6 +1,9 @@
 """GPU tests of the row operators against their float64 oracle: whole numbers bit-exact, floating
 outputs within bounds that count the roundings (each is derived where it is used)."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,7 @@ from oracle import moe_ref, rows_ref
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 F32, BF16 = B.MOE_FMT_F32, B.MOE_FMT_BF16
 DT = {F32: torch.float32, BF16: torch.bfloat16}
 EPS = 2.0 ** -24                    # half a step of float32
@@ -208,6 +212,33 @@ def test_route_strided_rows_at_odd_addresses(dtype, pad):
     view.copy_(dev(rng.standard_normal((89, 64)), dtype))
     kw = dict(top_k=8, norm=True)
     check_route(view, route_on_gpu(view, **kw), **kw)
+
+
+def test_route_past_two_to_the_31_logits():
+    """The last rows of a long batch route and group like the same rows alone."""
+    rows, E = 4_300_000, 512
+    g = torch.Generator(device="cuda").manual_seed(2)
+    part = torch.randn(1000, E, device="cuda", generator=g)
+    l = part.repeat(rows // 1000, 1)
+    kw = dict(top_k=2, routing="softmax", norm=True)
+    few, many = route_on_gpu(part, **kw), route_on_gpu(l, **kw)
+    n = rows // 1000
+    np.testing.assert_array_equal(many["expert_offsets"], few["expert_offsets"] * n)
+    np.testing.assert_array_equal(many["idx"].reshape(n, -1), np.repeat(few["idx"].reshape(1, -1), n, axis=0))
+    perm, pairs = many["token_to_perm"].astype(np.int64), many["sorted_pairs"]
+    np.testing.assert_array_equal(pairs[perm], np.arange(2 * rows))
+    flat = many["idx"].reshape(-1)[pairs]             # grouped, and in order within each expert
+    assert np.all(np.diff(flat) >= 0) and np.all(np.diff(pairs)[np.diff(flat) == 0] > 0)
+
+
+def test_route_without_grouping_needs_no_workspace():
+    l = torch.randn(100, 40, device="cuda")
+    idx, w = torch.empty(100, 3, dtype=torch.int32, device="cuda"), torch.empty(100, 3, device="cuda")
+    cfg = B.moe_route_cfg(num_experts=40, top_k=3, routing=0, norm_topk_prob=1, select_on_raw_logits=0,
+                          has_expert_bias=0, routed_scaling_factor=1.0, num_groups=1, topk_groups=1, group_score=0,
+                          logits_dtype=F32)
+    B.moe_route_rows(cfg, 100, l, 40, None, idx, w, stream=torch.cuda.current_stream())
+    assert torch.equal(idx.long(), torch.topk(l, 3, dim=1).indices)
 
 
 def test_route_agrees_with_the_decode_layer():
@@ -418,7 +449,7 @@ def test_product_row_counts(rows, n, k):
 
 
 @pytest.mark.parametrize("act", [None, "swiglu", "geglu"])
-@pytest.mark.parametrize("rows,n,k", [(1, 1, 16), (3, 65, 48), (5, 127, 144), (40, 130, 2064), (130, 257, 1008),
+@pytest.mark.parametrize("rows,n,k", [(1, 1, 16), (90, 1, 16), (3, 65, 48), (5, 127, 144), (40, 130, 2064), (130, 257, 1008),
                                       (270, 384, 512), (20, 1000, 4096), (600, 100, 128)])
 def test_product_odd_sizes(rows, n, k, act):
     for dt in (F32, BF16):
@@ -540,6 +571,43 @@ def test_product_rows_do_not_depend_on_their_neighbours():
         np.testing.assert_array_equal(q.run()[0], many[r])
 
 
+def test_product_output_past_two_to_the_31_elements():
+    rows, n, k = 70_001, 32_768, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randint(-127, 128, (rows, k), device="cuda", generator=g, dtype=torch.int8)
+    w = torch.randint(-127, 128, (1, n, k), device="cuda", generator=g, dtype=torch.int8)
+    xs, ws = torch.ones(rows, device="cuda"), torch.ones(1, n, device="cuda")
+    out = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    cfg = B.moe_matmul_cfg(n=n, k=k, num_experts=1, top_k=1, activation=0, out_dtype=BF16)
+    work = workspace(B.moe_matmul_workspace_bytes(cfg, rows))
+    B.moe_matmul_int8(cfg, rows, x, k, xs, rows, None, None, None, int8_matrix(w, ws), None, out, n, work,
+                      work.numel(), torch.cuda.current_stream())
+    # sums of 16 products of integers are exact in float32
+    at = torch.tensor([0, 1, 32_767, 65_535, 65_536, rows - 2, rows - 1], device="cuda")
+    want = (x[at].float() @ w[0].float().t()).bfloat16()
+    assert torch.equal(out[at], want) and status(work) == B.MOE_OK
+
+
+def test_product_weights_past_two_to_the_31_bytes():
+    E, n, k = 68, 4096, 8192
+    w = torch.zeros(E, n, k, dtype=torch.int8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w[-1] = torch.randint(-127, 128, (n, k), device="cuda", generator=g, dtype=torch.int8)
+    x = torch.randint(-127, 128, (150, k), device="cuda", generator=g, dtype=torch.int8)
+    xs, ws = torch.ones(150, device="cuda"), torch.ones(E, n, device="cuda")
+    for rows in (3, 150):
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[-1] = rows
+        out = torch.empty(rows, n, device="cuda")
+        cfg = B.moe_matmul_cfg(n=n, k=k, num_experts=E, top_k=1, activation=0, out_dtype=F32)
+        work = workspace(B.moe_matmul_workspace_bytes(cfg, rows))
+        B.moe_matmul_int8(cfg, rows, x, k, xs, rows, off, None, None, int8_matrix(w, ws), None, out, n, work,
+                          work.numel(), torch.cuda.current_stream())
+        want = (x[:rows].double() @ w[-1].double().t())
+        # one rounding of the exact sum
+        assert torch.all((out.double() - want).abs() <= EPS * want.abs())
+
+
 # ---- blend ---------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("y_dtype", [F32, BF16])
@@ -587,6 +655,25 @@ def test_combine_skips_rows_it_does_not_name():
     B.moe_combine_rows(2, 32, 2, F32, y, 32, 8, dev(np.array([3, -1, -1, -1], np.int32)), None, None, 0, None,
                        F32, out, 32, torch.cuda.current_stream())
     assert torch.all(out[0] == 2) and torch.all(out[1] == 0)
+
+
+def test_combine_without_any_row_of_y():
+    sh = torch.randn(3, 24, device="cuda")
+    out = torch.empty(3, 24, device="cuda")
+    perm = torch.full((6,), -1, dtype=torch.int32, device="cuda")
+    B.moe_combine_rows(3, 24, 2, F32, None, 24, 0, perm, None, sh, 24, None, F32, out, 24, torch.cuda.current_stream())
+    assert torch.equal(out, sh)
+
+
+def test_combine_past_two_to_the_31_elements():
+    rows, n = 66_000, 32_776
+    y = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    y[-1] = torch.randn(n, device="cuda")
+    y[-2] = torch.randn(n, device="cuda")
+    perm = torch.tensor([rows - 1, rows - 2], dtype=torch.int32, device="cuda")
+    out = torch.empty(1, n, device="cuda")
+    B.moe_combine_rows(1, n, 2, BF16, y, n, rows, perm, None, None, 0, None, F32, out, n, torch.cuda.current_stream())
+    assert torch.equal(out[0], y[-1].float() + y[-2].float())
 
 
 def test_combine_more_rows_than_a_grid_axis_holds():
@@ -710,6 +797,30 @@ def test_layer_captured_and_replayed():
         torch.cuda.synchronize()
         for n, t in want.items():
             assert torch.equal(getattr(L, n), t), n
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing has to be called before a capture: the library's own set-up is no work on a stream."""
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+from test_row_ops_gpu import Layer
+L = Layer(70, 256, 128, 16, 4)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    L.forward(torch.cuda.current_stream())
+graph.replay()
+torch.cuda.synchronize()
+got = L.out.clone()
+L.forward()
+torch.cuda.synchronize()
+assert torch.equal(got, L.out) and bool(L.out.any())
+print("captured")
+""" % (ROOT, os.path.join(ROOT, "tests"))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_layers_on_two_streams_at_once():
