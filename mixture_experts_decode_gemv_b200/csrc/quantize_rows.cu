@@ -11,7 +11,7 @@
 // the threads that read it (32, 128 or 512 of them, eight elements to a load) between the pass for its
 // maximum and the pass that rounds. The ordinary element costs five instructions: the quotient rounded
 // by adding 1.5 * 2^23 in the fma that forms it, the remainder, and its largest magnitude so far; only
-// where that reaches half a scale are the group's eight elements rounded again with care.
+// where that reaches half a scale are the group's eight elements looked at again.
 #include "host.h"
 #include "rows.cuh"
 
@@ -84,8 +84,9 @@ struct Eight {
   }
 };
 
-// Codes of eight elements.
-__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float scale, float inv, float half) {
+// Codes of eight elements. `far_limit` is half a scale, or infinity where the scale is a power of two: then
+// the reciprocal, the quotients and their rounding are exact, ties (which such rows are full of) included.
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float scale, float inv, float half, float far_limit) {
   constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
   float t[8], far = 0.f;
 #pragma unroll
@@ -93,13 +94,19 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float scale, floa
     t[i] = fmaf(v[i], inv, kRound);
     far = fmaxf(far, fabsf(fmaf(kRound - t[i], scale, v[i])));
   }
+  if (far >= far_limit) {
+    // one step towards the remainder where it is over half a scale, or is half and the code odd. (bf16 rows
+    // come here for every element that is half of their largest.)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = fmaf(kRound - t[i], scale, v[i]);
+      const bool odd = __float_as_uint(t[i]) & 1u;
+      if (fabsf(r) > half || (fabsf(r) == half && odd)) t[i] += copysignf(1.0f, r);
+    }
+  }
   uint32_t q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(t[i]);
-  if (far >= half) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = (uint32_t)quantise(v[i], scale, inv, half);
-  }
   auto pack = [](uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
   };
@@ -140,6 +147,7 @@ quantize_vectors_kernel(long long rows, int groups, const uint8_t* x, long long 
   const float scale = scale_of(top);
   const bool bad = top >= 0x7f800000u;
   const float inv = __fdiv_rn(1.0f, scale), half = 0.5f * scale;
+  const float far_limit = (__float_as_uint(scale) & 0x7fffffu) == 0u ? INFINITY : half;
   if (t == 0) scales[row] = scale;
   int8_t* out = codes + row * ld_codes;
 #pragma unroll
@@ -148,7 +156,7 @@ quantize_vectors_kernel(long long rows, int groups, const uint8_t* x, long long 
     if (g < groups) {
       float v[8];
       e[j].values(v);
-      const uint2 q = codes_of(v, scale, inv, half);
+      const uint2 q = codes_of(v, scale, inv, half, far_limit);
       *(uint2*)(out + (size_t)g * 8) = bad ? make_uint2(0, 0) : q;
     }
   }
