@@ -55,7 +55,7 @@ struct RouteArgs {
 // Order-preserving map of a float key to uint32; every key that can be selected maps above 0.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
@@ -253,10 +253,12 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, const Place& at, lo
 #pragma unroll
     for (int j = 0; j < NJ; ++j) lg[j] = at.real(a, j) ? load_one(a.logits, row + at.base + j, a.f32) : -INFINITY;
   }
+  // NaN becomes -infinity (the larger of the two), +infinity the largest finite number
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const bool live = lg[j] > -INFINITY && bs[j] > -INFINITY;   // NaN compares false
-    lg[j] = live ? fminf(lg[j], FLT_MAX) : -INFINITY;
+  for (int j = 0; j < NJ; ++j) lg[j] = fminf(fmaxf(lg[j], -INFINITY), FLT_MAX);
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) lg[j] = bs[j] > -INFINITY ? lg[j] : -INFINITY;   // NaN compares false
   }
 }
 
@@ -388,8 +390,7 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
   sort_lane<NJ>(key, id);
 
   out.id = -1;
-  float prev = 0.f;
-  int prev_id = 0;
+  uint32_t found = 0u;                               // key of this lane's slot
   const int rounds = a.k + (a.bias ? 1 : 0);         // with computed keys the first loser's gap counts too
 #pragma unroll 1
   for (int s = 0; s < rounds; ++s) {
@@ -397,19 +398,10 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
     if (win == 0u) break;                            // no expert is left
     const int owner = __ffs(__ballot_sync(kFull, key[0] == win)) - 1;
     const int got = __shfl_sync(kFull, id[0], owner);
-    if (a.bias) {
-      const float v = unordered(win);
-      if (s > 0 && prev - v <= tol) {
-        // equal logits with equal biases tie in any arithmetic
-        const size_t row = (size_t)r * (size_t)a.ld;
-        if (load_one(a.logits, row + got, a.f32) != load_one(a.logits, row + prev_id, a.f32) ||
-            a.bias_p[got] != a.bias_p[prev_id])
-          ordered_ok = false;
-      }
-      prev = v;
-      prev_id = got;
+    if (lane == s) {
+      out.id = got;
+      found = win;
     }
-    if (lane == s) out.id = got;
     if (lane == owner) {
 #pragma unroll
       for (int j = 0; j + 1 < NJ; ++j) {
@@ -419,9 +411,25 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
       key[NJ - 1] = 0u;
     }
   }
-  if (!ordered_ok) {   // the experts found are those of the first k + 1 places if the next is clearly below
-    const uint32_t next = __reduce_max_sync(kFull, key[0]);
-    if (next && prev - unordered(next) <= tol) sure = false;
+  if (a.bias) {
+    // gaps between neighbours in the order found
+    const uint32_t above = __shfl_up_sync(kFull, found, 1);
+    const int above_id = __shfl_up_sync(kFull, out.id, 1);
+    bool close = lane > 0 && found != 0u && unordered(above) - unordered(found) <= tol;
+    if (__any_sync(kFull, close)) {
+      if (close) {   // equal logits with equal biases tie in any arithmetic
+        const size_t row = (size_t)r * (size_t)a.ld;
+        close = load_one(a.logits, row + out.id, a.f32) != load_one(a.logits, row + above_id, a.f32) ||
+                a.bias_p[out.id] != a.bias_p[above_id];
+      }
+      if (__any_sync(kFull, close)) {
+        // the experts found are those of the first k + 1 places if the next is clearly below
+        ordered_ok = false;
+        const uint32_t next = __reduce_max_sync(kFull, key[0]);
+        const uint32_t last = __shfl_sync(kFull, found, a.k);
+        if (next && unordered(last) - unordered(next) <= tol) sure = false;
+      }
+    }
   }
   return !sure ? kOpen : ordered_ok ? kSure : kOrderOpen;
 }
