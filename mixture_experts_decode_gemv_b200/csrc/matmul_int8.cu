@@ -314,13 +314,13 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
     prefetch_map(&map_w);
     prefetch_map(&map_up);
   }
-  release_next();
-  wait_previous();
-  list_tiles<kPairN>(a, sh.list);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  release_next();
+  wait_previous();   // all of the above may overlap the kernel before
+  list_tiles<kPairN>(a, sh.list);
   const uint32_t tmem = sh.tmem;
   const int first = blockIdx.x / 2, stride = gridDim.x / 2;
   volatile int* abort = &sh.abort;
@@ -608,13 +608,13 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     prefetch_map(&map_w);
     prefetch_map(&map_up);
   }
-  release_next();
-  wait_previous();
-  list_tiles<kFewN>(a, sh.list);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  release_next();
+  wait_previous();   // all of the above may overlap the kernel before
+  list_tiles<kFewN>(a, sh.list);
   const uint32_t tmem = sh.tmem;
   const int first = blockIdx.x / split, stride = gridDim.x / split;
   volatile int* abort = &sh.abort;
@@ -928,10 +928,10 @@ cudaError_t launch_clusters(void (*kernel)(P...), long long clusters, int size, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Tiles of a call at most: every expert may end in a tile that is not full.
+// Tiles of a call at most: an expert with r > 0 rows has at most 1 + (r - 1) / `rows` row tiles.
 long long most_tiles(const MatmulArgs& a, int rows, int channels) {
-  const long long experts = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : 0;
-  return ((a.rows + rows - 1) / rows + experts) * ((a.n + channels - 1) / channels);
+  const long long experts = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : 1;
+  return (experts + (a.rows - experts) / rows) * ((a.n + channels - 1) / channels);
 }
 
 // The tensor maps of a call; only those that its kernel reads are made.
@@ -964,24 +964,33 @@ cudaError_t launch_product(MatmulArgs& a, cudaStream_t st) {
     m.up = m.w;
   }
 
-  // Few rows: where an expert has about 16 rows or fewer (128 experts, 2 x 768 channels, k = 2048: 46, 61, 71,
-  // 77, 89 us with 1, 4, 8, 16, 32 rows an expert, against 50, 65, 75, 77, 80 in pairs), and up to one tile's
-  // 64 where the pairs' tiles would leave half of the device idle (64 rows, 5120 channels, k = 8192: 14.4
-  // against 18.1; 2 x 8192 channels, k = 5120, which fill it: 19.4 against 18.0).
+  // Which kernel, and how its k is split. Up to a tile's 64 rows an expert both are a pass over the weights, so
+  // the shorter longest block decides: rounds of tiles x the steps of a tile (16 KB of weights a block in both)
+  // and what the rest of a tile takes, in steps' time: 2 and one for each eight rows where the k steps of a tile
+  // are added up, 6 in pairs. Measured, us, few rows / pairs: 128 experts, 2 x 768 channels, k = 2048, with 1, 4,
+  // 8, 16, 32 rows an expert: 46 / 50, 61 / 65, 71 / 75, 77 / 77, 89 / 80. One matrix, 64 rows: 5120 channels,
+  // k = 8192: 14.4 / 18.1; 2 x 8192 channels, k = 5120: 19.4 / 18.0. One row, k = 8192, 10240 and 20480 channels: 19.2
+  // and 41.5 in single blocks, 17.3 and 28.7 with the splits that this gives.
+  const int steps = (a.k + kStep - 1) / kStep;
   const long long per = a.rows / (a.offsets ? a.experts : 1);   // rows of an expert, if they were even
   const long long pair_tiles = most_tiles(a, kPairN, ACT ? 128 : 256), few_tiles = most_tiles(a, kFewN, ACT ? 64 : 128);
   if (pair_tiles > 0x7fffffffLL || few_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;   // more output than any device holds
-  if (per <= 16 || (per <= kFewN && 2 * pair_tiles <= pairs)) {
-    const int steps = (a.k + kStep - 1) / kStep;
-    // the largest split whose clusters all run at once
-    int size = steps < kFewMaxCluster ? steps : kFewMaxCluster;
-    for (; size >= 1; --size) {
+  if (per <= kFewN) {
+    int best = 0, best_clusters = 1;
+    long long best_cost = (pair_tiles + pairs - 1) / pairs * (steps + 6);
+    for (int size = 1; size <= kFewMaxCluster && size <= steps; ++size) {
       e = resident_clusters<matmul_few_kernel<ACT>>(dev, kFewThreads, kFewSmem, size, &clusters);
       if (e != cudaSuccess) return e;
-      if (size == 1 || few_tiles <= clusters) break;
+      const long long cost = (few_tiles + clusters - 1) / clusters * ((steps + size - 1) / size + 2 + per / 8);
+      if (cost < best_cost) {
+        best = size;
+        best_clusters = clusters;
+        best_cost = cost;
+      }
     }
-    return launch_clusters(matmul_few_kernel<ACT>, few_tiles < clusters ? few_tiles : clusters, size, kFewThreads,
-                           kFewSmem, st, a, m.w, m.up);
+    if (best)
+      return launch_clusters(matmul_few_kernel<ACT>, few_tiles < best_clusters ? few_tiles : best_clusters, best,
+                             kFewThreads, kFewSmem, st, a, m.w, m.up);
   }
   if (a.pairs) m.x = m.w;   // gathered rows go without a map
   else if (!map_rows(&m.x, a.x, a.k, a.x_rows, a.ld_x, kRowBox)) return cudaErrorInvalidValue;
