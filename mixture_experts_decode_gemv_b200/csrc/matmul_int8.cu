@@ -99,7 +99,7 @@ enum Act { kPlain, kSwiglu, kGeglu };
 template <int ACT>
 __device__ __forceinline__ float gated(float g, float u) {
   if constexpr (ACT == kGeglu) return moe::gelu_tanh_mul(g, u);
-  return __fdividef(g * u, 1.0f + __expf(-g));
+  return __fdividef(g, 1.0f + __expf(-g)) * u;   // not g * u first: that may overflow where the gate is shut
 }
 
 // The row tiles of all experts, in expert order.

@@ -560,6 +560,21 @@ def test_product_wait_that_runs_out(rows, gather):
     p.check(p.run())
 
 
+@pytest.mark.parametrize("rows", [3, 90])
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+def test_product_of_a_shut_gate_is_zero_however_large(rows, act):
+    """A gate far below zero times an up as large: their product passes float32, the activation is 0."""
+    p = Product(13, rows, 64, 64, act=act, out_dtype=F32)
+    p.dx.fill_(1)
+    p.dw[0].fill_(-1)
+    p.dw[1].fill_(1)
+    p.dxs.fill_(1e12)
+    for s in p.dws:
+        s.fill_(1e12)
+    got = p.run()
+    assert np.all(got == 0)
+
+
 def test_product_rows_do_not_depend_on_their_neighbours():
     """A row's bits are the same alone and within any batch."""
     p = Product(6, 300, 160, 528, out_dtype=F32)
