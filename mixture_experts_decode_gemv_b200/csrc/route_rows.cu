@@ -377,15 +377,20 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
       }
     }
     float of = a.top2 && m2 > -INFINITY ? m1 + m2 : m1;
-    of = __shfl_sync(kFull, of, min(at.g, a.G - 1) * a.lanes);
+    const int head = min(at.g, a.G - 1) * a.lanes;
+    of = __shfl_sync(kFull, of, head);
+    // a group takes part by its best value: the sum of two finite ones may pass the largest number
+    const float best = __shfl_sync(kFull, m1, head);
+    const bool some = at.g < a.G && best > -INFINITY;
     int rank = 0;
     for (int o = 0; o < a.G; ++o) {
       const float other = __shfl_sync(kFull, of, o * a.lanes);
       rank += other > of || (other == of && o < at.g);
     }
-    const bool some = at.g < a.G && of > -INFINITY;
     kept = some && rank < a.keep;
     if (sums || a.bias) {
+      // float32 does not rank infinite sums, and their distances are no numbers
+      if (__any_sync(kFull, some && !(fabsf(of) <= FLT_MAX))) sure = false;
       const float low = unordered(__reduce_min_sync(kFull, kept ? ordered(of) : ordered(INFINITY)));
       const uint32_t high = __reduce_max_sync(kFull, some && !kept ? ordered(of) : 0u);
       if (high && low - unordered(high) <= 2.0f * tol) sure = false;

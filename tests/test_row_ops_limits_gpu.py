@@ -1,0 +1,78 @@
+"""GPU tests of the row operators at the limits of their arguments: values at the ends of float32, lengths
+at the ends of 32 bits, and the batch sizes where the choice of a launch changes."""
+import numpy as np
+import pytest
+import torch
+
+from test_row_ops_gpu import check_route, dev, route_on_gpu
+
+pytestmark = pytest.mark.gpu
+
+F32_MAX = float(np.finfo(np.float32).max)
+BF16_MAX = float(torch.finfo(torch.bfloat16).max)
+
+
+def rows_at_the_ends(E, G, big, seed):
+    """Rows whose groups hold logits near +-big: alone, beside ordinary ones, and beside masked ones."""
+    rng = np.random.default_rng(seed)
+    size = E // G
+    l = rng.standard_normal((40, E)) * 1.5
+    of = np.arange(E) // size
+    l[0] = -big                                       # every pair of a group sums to -2 big
+    l[1, of == 0] = -big                              # a group switched off by the lowest finite number ...
+    l[2] = -np.inf
+    l[2, of == 1] = -big                              # ... and needed, as nothing else is left but
+    l[2, G // 2 * size] = 0.5                         # one expert
+    l[3] = -np.inf
+    l[3, of >= G - 2] = -big
+    l[4] = big
+    l[5, of % 2 == 1] = np.inf                        # as the largest finite logit
+    l[6, ::size] = 0.9 * big                          # sums past the largest number, the highest in the last group
+    l[6, 1::size] = big * np.linspace(0.3, 0.99, G)
+    l[7, ::size] = big                                # equal sums past it: the lower groups
+    l[7, 1::size] = big
+    l[8, ::size] = big                                # big - big
+    l[8, 1::size] = -big
+    l[8, 2::size] = -big
+    l[9] = np.where(rng.random(E) < 0.5, -big, l[9])
+    for r in range(10, 30):                           # sums on both sides of the border
+        l[r] = rng.uniform(-1.0, 1.0, E) * big
+    for r in range(30, 40):
+        l[r] = np.where(rng.random(E) < 0.7, -np.inf, rng.choice([-big, 0.75 * -big, 0.5 * -big], E))
+    return l
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,G,keep", [(32, 4, 2), (256, 8, 4), (510, 17, 5), (512, 32, 7)])
+@pytest.mark.parametrize("routing", ["sigmoid", "sqrtsoftplus"])
+def test_route_group_sums_past_float32(routing, E, G, keep, dtype):
+    """Groups are ranked by their sums as 64 bits hold them, and one with a finite logit is never masked."""
+    t = dev(rows_at_the_ends(E, G, F32_MAX if dtype == torch.float32 else BF16_MAX, E), dtype)
+    for score in ("top2", "max"):
+        kw = dict(top_k=6, routing=routing, norm=True, raw=True, groups=G, topk_groups=keep, group_score=score)
+        check_route(t, route_on_gpu(t, **kw), **kw)
+
+
+@pytest.mark.parametrize("E,G,keep", [(32, 4, 2), (256, 8, 4), (512, 32, 7)])
+@pytest.mark.parametrize("routing", ["sigmoid", "sqrtsoftplus"])
+def test_route_biases_at_the_ends_of_float32(routing, E, G, keep):
+    rng = np.random.default_rng(E)
+    size = E // G
+    l = rng.standard_normal((24, E)) * 1.5
+    l[4:8, size:] = -np.inf                           # only the first group is left
+    l[8:16] = np.where(rng.random((8, E)) < 0.8, -np.inf, l[8:16])
+    t = dev(l, torch.float32)
+    biases = []
+    b = rng.standard_normal(E) * 0.1
+    b[:size] = -F32_MAX                               # the first group switched off
+    biases.append(b)
+    b = rng.standard_normal(E) * 0.1
+    b[::size], b[1::size] = 0.9 * F32_MAX, F32_MAX * np.linspace(0.3, 0.99, G)
+    biases.append(b)
+    biases.append(np.full(E, -F32_MAX))
+    biases.append(np.where(np.arange(E) % size < 2, np.inf, 0.1 * rng.standard_normal(E)))
+    for b in biases:
+        for score in ("top2", "max"):
+            kw = dict(top_k=6, routing=routing, norm=True, bias=dev(b.astype(np.float32)), groups=G, topk_groups=keep,
+                      group_score=score)
+            check_route(t, route_on_gpu(t, **kw), **kw)
