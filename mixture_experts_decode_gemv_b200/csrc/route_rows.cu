@@ -264,9 +264,10 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, const Place& at, lo
 #pragma unroll
     for (int j = 0; j < NJ; ++j) lg[j] = at.real(a, j) ? load_one(a.logits, row + at.base + j, a.f32) : -INFINITY;
   }
-  // NaN becomes -infinity (the larger of the two), +infinity the largest finite number
+  // NaN becomes -infinity (the larger of the two), +infinity the largest finite number, and -0 becomes 0, which
+  // it ties with (keys are compared by their bits)
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) lg[j] = fminf(fmaxf(lg[j], -INFINITY), FLT_MAX);
+  for (int j = 0; j < NJ; ++j) lg[j] = fminf(fmaxf(lg[j], -INFINITY), FLT_MAX) + 0.0f;
   if (a.bias) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) lg[j] = bs[j] > -INFINITY ? lg[j] : -INFINITY;   // NaN compares false

@@ -76,3 +76,19 @@ def test_route_biases_at_the_ends_of_float32(routing, E, G, keep):
             kw = dict(top_k=6, routing=routing, norm=True, bias=dev(b.astype(np.float32)), groups=G, topk_groups=keep,
                       group_score=score)
             check_route(t, route_on_gpu(t, **kw), **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,G,keep", [(16, 1, 1), (160, 8, 3), (256, 1, 1), (510, 17, 5)])
+def test_route_zeros_of_both_signs_tie(E, G, keep, dtype):
+    rng = np.random.default_rng(E)
+    l = np.where(rng.random((50, E)) < 0.5, 0.0, -0.0)
+    l[25:] = np.where(rng.random((25, E)) < 0.9, l[25:], rng.integers(-1, 2, (25, E)))
+    t = dev(l, dtype)
+    assert bool(torch.signbit(t).any()) and not bool(torch.signbit(t).all())
+    zero = torch.zeros(E, device="cuda")
+    for kw in (dict(routing="softmax"), dict(routing="sigmoid", raw=True), dict(routing="sqrtsoftplus", bias=zero),
+               dict(routing="sigmoid", bias=-zero)):
+        for score in ("max", "top2"):
+            kw = dict(kw, top_k=6, norm=True, groups=G, topk_groups=keep, group_score=score)
+            check_route(t, route_on_gpu(t, **kw), **kw)
