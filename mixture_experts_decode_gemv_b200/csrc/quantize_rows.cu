@@ -172,10 +172,11 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(int k, bool f3
   wait_previous();
   const long long row = blockIdx.x;
   const size_t base = (size_t)row * (size_t)ld_x;
+  const unsigned n = k;   // positions unsigned: the last step may pass 2^31 - 1
   // magnitudes as integers: the order of their bits is theirs, and infinity and NaN are largest
   uint32_t top = 0;
 #pragma unroll 4
-  for (int j = threadIdx.x; j < k; j += kQThreads)
+  for (unsigned j = threadIdx.x; j < n; j += kQThreads)
     top = max(top, __float_as_uint(load_one(x, base + j, f32)) & 0x7fffffffu);
   top = __reduce_max_sync(kFull, top);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(int k, bool f3
   const float inv = __fdiv_rn(1.0f, scale), half = 0.5f * scale;
   int8_t* out = codes + (size_t)row * (size_t)ld_codes;
 #pragma unroll 4
-  for (int j = threadIdx.x; j < k; j += kQThreads)
+  for (unsigned j = threadIdx.x; j < n; j += kQThreads)
     out[j] = bad ? (int8_t)0 : (int8_t)quantise(load_one(x, base + j, f32), scale, inv, half);
   if (threadIdx.x == 0) scales[row] = scale;
 }

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_row_ops_gpu import check_route, dev, route_on_gpu
+from mixture_experts_decode_gemv_b200 import binding as B
+from test_row_ops_gpu import BF16, check_route, dev, route_on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +93,22 @@ def test_route_zeros_of_both_signs_tie(E, G, keep, dtype):
         for score in ("max", "top2"):
             kw = dict(kw, top_k=6, norm=True, groups=G, topk_groups=keep, group_score=score)
             check_route(t, route_on_gpu(t, **kw), **kw)
+
+
+def test_quantise_the_longest_row():
+    """A row of 2^31 - 1 elements: positions one step behind its end do not fit 31 bits."""
+    k = 2**31 - 1
+    x = torch.zeros(1, k, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 127, 128, 2**30, k - 129, k - 128, k - 2, k - 1], device="cuda")
+    v = torch.tensor([127.0, -1.0, 2.5, 3.5, -64.0, 5.0, -127.0, 100.0], device="cuda")     # the scale is 1
+    x[0, at] = v.bfloat16()
+    full = torch.full((k + 512,), 55, dtype=torch.int8, device="cuda")
+    scales = torch.full((3,), 77.0, device="cuda")
+    B.moe_quantize_rows_int8(1, k, BF16, x, k, full[256:256 + k], k, scales[1:2], torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert scales.tolist() == [77.0, 1.0, 77.0]
+    assert torch.all(full[:256] == 55) and torch.all(full[256 + k:] == 55)
+    codes = full[256:256 + k]
+    assert codes[at].tolist() == [127, -1, 2, 4, -64, 5, -127, 100]     # halves to even
+    codes[at] = 0
+    assert not torch.any(codes)
