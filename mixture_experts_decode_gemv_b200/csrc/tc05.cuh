@@ -48,13 +48,14 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrival on a barrier of any block of the cluster (a shared::cluster address). What it orders lies in
-// shared or tensor memory and was completed before by a proxy or tensor-memory fence; a release at
-// cluster scope would also wait for the thread's stores to global memory and its copies in flight.
+// Arrival on a barrier of any block of the cluster (a shared::cluster address), for use behind a proxy or
+// tensor-memory fence alone: that fence has completed what the arrival orders (rows that the tensor cores read,
+// loads from tensor memory), and its own release reaches no further than this block. A release at cluster
+// scope would also wait for the thread's stores to global memory and its copies in flight.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same, ordering the thread's stores into the other blocks' shared memory.
+// The same, ordering the warp's plain loads and stores of shared memory, its own and the other blocks'.
 __device__ __forceinline__ void bar_arrive_release(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from mixture_experts_decode_gemv_b200 import binding as B
-from test_row_ops_gpu import BF16, check_route, dev, route_on_gpu
+from test_row_ops_gpu import BF16, F32, Product, check_route, dev, route_on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,15 @@ def test_quantise_the_longest_row():
     assert codes[at].tolist() == [127, -1, 2, 4, -64, 5, -127, 100]     # halves to even
     codes[at] = 0
     assert not torch.any(codes)
+
+
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("rows", [1, 7, 64])
+def test_product_exchanges_the_sums_of_many_tiles(rows, act):
+    """A long k split over clusters that take several tiles each: the blocks' sums change hands tile after tile in
+    the same shared memory."""
+    p = Product(rows, rows, 20480 if act is None else 10240, 8192, act=act, out_dtype=F32)
+    first = p.run()
+    p.check(first)
+    for _ in range(20):
+        np.testing.assert_array_equal(p.run(), first)
