@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kCThreads) combine_rows_kernel(const __grid_co
 template <typename Y, typename O, int VEC>
 cudaError_t launch_combine(CombineArgs a, cudaStream_t st) {
   constexpr int U = 16 / (int)(VEC * sizeof(Y));
-  a.lanes = (a.n / VEC + U - 1) / U;
+  a.lanes = (a.n / VEC - 1) / U + 1;   // at most 2^31 / U, so that a thread's vectors stay below 2^31
   const long long blocks = (a.rows * a.lanes + kCThreads - 1) / kCThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;   // more output than any device holds
   cudaLaunchConfig_t cfg = {};

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from mixture_experts_decode_gemv_b200 import binding as B
-from test_row_ops_gpu import BF16, F32, Product, check_route, dev, route_on_gpu
+from test_row_ops_gpu import BF16, DT, F32, Product, check_route, dev, route_on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,22 @@ def test_product_exchanges_the_sums_of_many_tiles(rows, act):
     p.check(first)
     for _ in range(20):
         np.testing.assert_array_equal(p.run(), first)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_combine_the_longest_row(dtype):
+    n = 2**31 - 1
+    y = torch.zeros(1, n, dtype=DT[dtype], device="cuda")
+    at = torch.tensor([0, 1, 2**28, 2**30 + 1, n - 9, n - 8, n - 2, n - 1], device="cuda")
+    y[0, at] = torch.arange(1, 9, device="cuda").to(DT[dtype])
+    perm = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.full((1,), 2.0, device="cuda")
+    full = torch.full((n + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.moe_combine_rows(1, n, 1, dtype, y, n, 1, perm, w, None, 0, None, BF16, full[64:64 + n], n,
+                       torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert torch.all(full[:64] == 7) and torch.all(full[64 + n:] == 7)
+    out = full[64:64 + n]
+    assert torch.equal(out[at].float(), 2.0 * torch.arange(1, 9, device="cuda"))
+    out[at] = 0
+    assert not torch.any(out)
