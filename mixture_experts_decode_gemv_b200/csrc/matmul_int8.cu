@@ -291,7 +291,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   constexpr int kChPair = ACT ? 128 : 256, kChBlock = kChPair / 2;
-  const int ch_tiles = (a.n + kChPair - 1) / kChPair;
+  const int ch_tiles = (a.n - 1) / kChPair + 1;   // the last one's channels stay below 2^31
   const int k_steps = (a.k + kStep - 1) / kStep;
 
   if (tid == 0) {
@@ -591,7 +591,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int split = (int)cluster_size(), rank = (int)cluster_rank();
   constexpr int kCh = ACT ? 64 : 128;
-  const int ch_tiles = (a.n + kCh - 1) / kCh;
+  const int ch_tiles = (a.n - 1) / kCh + 1;
   const int all_steps = (a.k + kStep - 1) / kStep;
   const int k_first = all_steps * rank / split, k_steps = all_steps * (rank + 1) / split - k_first;
 
@@ -948,7 +948,7 @@ cudaError_t launch_clusters(void (*kernel)(P...), long long clusters, int size, 
 // Tiles of a call at most: an expert with r > 0 rows has at most 1 + (r - 1) / `rows` row tiles.
 long long most_tiles(const MatmulArgs& a, int rows, int channels) {
   const long long experts = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : 1;
-  return (experts + (a.rows - experts) / rows) * ((a.n + channels - 1) / channels);
+  return (experts + (a.rows - experts) / rows) * ((a.n - 1) / channels + 1);
 }
 
 // The tensor maps of a call; only those that its kernel reads are made.

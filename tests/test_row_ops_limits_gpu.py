@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from mixture_experts_decode_gemv_b200 import binding as B
-from test_row_ops_gpu import BF16, DT, F32, Product, check_route, dev, route_on_gpu
+from test_row_ops_gpu import BF16, DT, F32, Product, check_route, dev, int8_matrix, route_on_gpu, status, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,29 @@ def test_combine_the_longest_row(dtype):
     assert torch.equal(out[at].float(), 2.0 * torch.arange(1, 9, device="cuda"))
     out[at] = 0
     assert not torch.any(out)
+
+
+@pytest.mark.parametrize("n", [2**31 - 1, 2**31 - 100, 2**31 - 200])
+def test_product_of_almost_two_to_the_31_channels(n):
+    k, rows = 16, 2
+    w = torch.zeros(n * k, dtype=torch.int8, device="cuda").view(1, n, k)
+    ws = torch.ones(1, n, device="cuda")
+    at = torch.cat([torch.arange(300), 2**30 + torch.arange(300), n - 300 + torch.arange(300)]).cuda()
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w[0, at] = torch.randint(-127, 128, (900, k), device="cuda", generator=g, dtype=torch.int8)
+    x = torch.randint(-127, 128, (rows, k), device="cuda", generator=g, dtype=torch.int8)
+    xs = torch.ones(rows, device="cuda")
+    full = torch.full((rows * n + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+    cfg = B.moe_matmul_cfg(n=n, k=k, num_experts=1, top_k=1, activation=0, out_dtype=BF16)
+    work = workspace(B.moe_matmul_workspace_bytes(cfg, rows))
+    B.moe_matmul_int8(cfg, rows, x, k, xs, rows, None, None, None, int8_matrix(w, ws), None, full[64:], n, work,
+                      work.numel(), torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert status(work) == B.MOE_OK
+    assert torch.all(full[:64] == 7) and torch.all(full[64 + rows * n:] == 7)
+    for r in range(rows):
+        out = full[64 + r * n:64 + (r + 1) * n]
+        # sums of 16 products of integers are exact in float32
+        assert torch.equal(out[at], (w[0, at].float() @ x[r].float()).bfloat16())
+        out[at] = 0
+        assert not torch.any(out)
