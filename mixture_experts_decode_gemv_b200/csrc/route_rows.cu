@@ -67,7 +67,13 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 }
 
 __device__ __forceinline__ float score_of(int routing, float l) {
-  if (routing == MOE_ROUTE_SQRTSOFTPLUS) return sqrtf(fmaxf(l, 0.f) + log1pf(expf(-fabsf(l))));
+  if (routing == MOE_ROUTE_SQRTSOFTPLUS) {
+    // far below zero softplus(l) = e^l (its next term is under 2^-24 of it), whose root float32 holds where it no longer
+    // holds e^l
+    const bool low = l < -17.0f;
+    const float e = expf(low ? 0.5f * l : -fabsf(l));
+    return low ? e : sqrtf(fmaxf(l, 0.f) + log1pf(e));
+  }
   return 1.0f / (1.0f + expf(-l));
 }
 

@@ -169,3 +169,19 @@ def test_product_of_almost_two_to_the_31_channels(n):
         assert torch.equal(out[at], (w[0, at].float() @ x[r].float()).bfloat16())
         out[at] = 0
         assert not torch.any(out)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("norm", [False, True])
+def test_route_roots_of_scores_below_float32(norm, dtype):
+    """sqrt(softplus(l)) is a normal number down to l = -174, where e^l has long left float32."""
+    l = np.stack([-87.0 - 0.5 * np.arange(64), -16.0 - 0.05 * np.arange(64), -100.0 - np.arange(64),
+                  np.where(np.arange(64) % 9 == 0, -16.5, -110.0 + 0.25 * np.arange(64)),
+                  np.random.default_rng(1).uniform(-120.0, -90.0, 64)])
+    t = dev(l, dtype)
+    zero = torch.zeros(64, device="cuda")
+    for kw in (dict(), dict(raw=True, groups=8, topk_groups=3, group_score="top2"), dict(bias=zero),
+               dict(groups=8, topk_groups=3, group_score="top2"),
+               dict(bias=zero, groups=8, topk_groups=3, group_score="top2")):
+        kw = dict(kw, top_k=16, routing="sqrtsoftplus", norm=norm)
+        check_route(t, route_on_gpu(t, **kw), **kw)
