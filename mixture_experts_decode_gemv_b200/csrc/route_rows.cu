@@ -7,9 +7,9 @@
 // id. A selection round is one warp maximum over the lanes' best keys.
 //
 // Decisions are those of 64-bit arithmetic. Logits compare exactly as they are. A computed key
-// (score + bias) or group score (a sum) carries rounding of a few 2^-24 of the magnitudes that it is
-// made of; when two that decide something lie within 2^-20 of those magnitudes, the row is routed
-// again with float64 scores (a few rows in a thousand).
+// (score + bias) or group score (a sum) carries rounding of a few 2^-24 of the largest score and of the
+// magnitudes that it is made of; when two that decide something lie closer than such errors may add up to
+// (2^-20 of the one, 3 * 2^-24 of the other), the row is settled in float64 (a few rows in a thousand).
 //
 // Bound by issue slots (69 % active, 13.8 M warp instructions): 8191 rows of 256 experts, best 4 of 8 groups, top 8
 // with a bias, take 24 us, 6 of them the grouping; the logits alone would take 1.4 from HBM. A row that is settled in
@@ -309,13 +309,14 @@ __device__ __forceinline__ void sort_lane(uint32_t (&key)[NJ], int (&id)[NJ]) {
 enum Verdict { kSure, kOrderOpen, kOpen };
 
 // Routes one row with float32 scores and tells which decisions hang on their rounding: none, the order of
-// the experts found (k + 1 of them, one to a lane), or more. Each key
-// and group score is within `tol` of its value (fast exponential and reciprocal: 4 units of 2^-23 of a
-// score, and the sums' roundings; 16 units of 2^-24 of the largest magnitudes are allowed, 64 for
-// softmax, whose scores carry the denominator's rounding too).
+// the experts found (k + 1 of them, one to a lane), or more. A score is off by at most 4 units of 2^-23 of the
+// largest (fast exponential and reciprocal; 16 for softmax, whose scores carry the denominator's rounding too), and
+// every sum by half a unit of its own: a large bias opens nothing but what it enters. What lies below the lower of two
+// keys that are apart is apart from the higher one too: a key and its error grow together.
+constexpr float kSumErr = 0x1.8p-23f;   // of the sums in two keys, or in a group's score and its border, relative to their magnitudes
 template <int NJ>
 __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at, long long r, const float (&lg)[NJ],
-                                          const float (&bs)[NJ], float most_bias, Slots& out) {
+                                          const float (&bs)[NJ], Slots& out) {
   const int lane = threadIdx.x & 31;
   const bool limited = a.keep < a.G, soft = a.routing == MOE_ROUTE_SOFTMAX;
   const bool sums = limited && a.top2;               // group scores are sums of values
@@ -337,7 +338,7 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
     inv = __fdividef(1.0f, out.den);
   }
   float sc[NJ];        // scores, where they decide something
-  float mag = 1.f;     // their largest magnitude
+  float mag = scored ? 1.f : 0.f;   // their largest magnitude
   if (scored) {
     if (soft) {
 #pragma unroll
@@ -354,13 +355,8 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
       }
       mag = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
     }
-  } else if (sums) {
-    mag = 0.f;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) mag = fmaxf(mag, lg[j] > -INFINITY ? fabsf(lg[j]) : 0.f);
-    mag = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
   }
-  const float tol = (mag + most_bias) * (soft ? 0x1p-18f : 0x1p-20f);
+  const float score_err = mag * (soft ? 0x1p-18f : 0x1p-20f);   // of two scores
   float kf[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) kf[j] = a.bias && lg[j] > -INFINITY ? sc[j] + bs[j] : lg[j];
@@ -383,12 +379,12 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
         m1 = fmaxf(m1, o1);
       }
     }
-    float of = a.top2 && m2 > -INFINITY ? m1 + m2 : m1;
     const int head = min(at.g, a.G - 1) * a.lanes;
-    of = __shfl_sync(kFull, of, head);
+    m1 = __shfl_sync(kFull, m1, head);
+    m2 = __shfl_sync(kFull, m2, head);
     // a group takes part by its best value: the sum of two finite ones may pass the largest number
-    const float best = __shfl_sync(kFull, m1, head);
-    const bool some = at.g < a.G && best > -INFINITY;
+    const bool some = at.g < a.G && m1 > -INFINITY, two = a.top2 && m2 > -INFINITY;
+    const float of = two ? m1 + m2 : m1;
     int rank = 0;
     for (int o = 0; o < a.G; ++o) {
       const float other = __shfl_sync(kFull, of, o * a.lanes);
@@ -396,11 +392,12 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
     }
     kept = some && rank < a.keep;
     if (sums || a.bias) {
-      // float32 does not rank infinite sums, and their distances are no numbers
-      if (__any_sync(kFull, some && !(fabsf(of) <= FLT_MAX))) sure = false;
-      const float low = unordered(__reduce_min_sync(kFull, kept ? ordered(of) : ordered(INFINITY)));
-      const uint32_t high = __reduce_max_sync(kFull, some && !kept ? ordered(of) : 0u);
-      if (high && low - unordered(high) <= 2.0f * tol) sure = false;
+      // float32 does not rank infinite sums
+      const bool infinite = !(fabsf(of) <= FLT_MAX);
+      const float err = score_err + (fabsf(m1) + (two ? fabsf(m2) : 0.f)) * kSumErr;
+      const uint32_t low = __reduce_min_sync(kFull, !kept ? ~0u : infinite ? 0u : ordered(of - err));
+      const uint32_t high = __reduce_max_sync(kFull, !some || kept ? 0u : infinite ? ~0u : ordered(of + err));
+      if (high >= low) sure = false;
     }
   }
   uint32_t key[NJ];
@@ -438,7 +435,8 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
     // gaps between neighbours in the order found
     const uint32_t above = __shfl_up_sync(kFull, found, 1);
     const int above_id = __shfl_up_sync(kFull, out.id, 1);
-    bool close = lane > 0 && found != 0u && unordered(above) - unordered(found) <= tol;
+    auto near = [&](float x, float y) { return x - y <= score_err + fmaxf(fabsf(x), fabsf(y)) * kSumErr; };
+    bool close = lane > 0 && found != 0u && near(unordered(above), unordered(found));
     if (__any_sync(kFull, close)) {
       if (close) {   // equal logits with equal biases tie in any arithmetic
         const size_t row = (size_t)r * (size_t)a.ld;
@@ -450,7 +448,7 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
         ordered_ok = false;
         const uint32_t next = __reduce_max_sync(kFull, key[0]);
         const uint32_t last = __shfl_sync(kFull, found, a.k);
-        if (next && unordered(last) - unordered(next) <= tol) sure = false;
+        if (next && near(unordered(last), unordered(next))) sure = false;
       }
     }
   }
@@ -495,18 +493,19 @@ __device__ __forceinline__ void route_block(const RouteArgs& a, long long first,
                                             int* s_count) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Place at(a);
-  float bs[NJ], most_bias = 0.f;
+  float bs[NJ];
+  auto load_bias = [&] {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    bs[j] = a.bias && at.real(a, j) ? a.bias_p[at.base + j] : 0.f;
-    if (bs[j] > -INFINITY) most_bias = fmaxf(most_bias, fabsf(bs[j]));
-  }
-  most_bias = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(most_bias)));
+    for (int j = 0; j < NJ; ++j) bs[j] = a.bias && at.real(a, j) ? a.bias_p[at.base + j] : 0.f;
+  };
+  // sixteen and more would be spilled between the rows
+  if (NJ < 16) load_bias();
   for (long long r = first + warp; r < last; r += kRWarps) {
+    if (NJ >= 16) load_bias();
     float lg[NJ];
     load_row<NJ>(a, at, r, bs, lg);
     Slots s;
-    const Verdict v = route_row<NJ>(a, at, r, lg, bs, most_bias, s);
+    const Verdict v = route_row<NJ>(a, at, r, lg, bs, s);
     if (v == kOrderOpen) settle_order(a, r, a.k + 1, s);
     else if (v == kOpen) route_row_f64<NJ>(a, r, s);
     if (lane >= a.k) s.id = -1;

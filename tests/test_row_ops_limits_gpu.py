@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from mixture_experts_decode_gemv_b200 import binding as B
+from oracle import rows_ref
 from test_row_ops_gpu import BF16, DT, F32, Product, check_route, dev, int8_matrix, route_on_gpu, status, workspace
 
 pytestmark = pytest.mark.gpu
@@ -185,3 +186,69 @@ def test_route_roots_of_scores_below_float32(norm, dtype):
                dict(bias=zero, groups=8, topk_groups=3, group_score="top2")):
         kw = dict(kw, top_k=16, routing="sqrtsoftplus", norm=norm)
         check_route(t, route_on_gpu(t, **kw), **kw)
+
+
+@pytest.mark.parametrize("routing", ["sigmoid", "sqrtsoftplus"])
+@pytest.mark.parametrize("E,G,keep", [(256, 1, 1), (320, 4, 2), (512, 8, 4), (510, 17, 5), (512, 32, 7)])
+def test_route_close_keys_among_large_biases(routing, E, G, keep):
+    """Keys that only 64 bits tell apart, beside experts whose biases are far from them on either side."""
+    rng = np.random.default_rng(E + G)
+    base = (rng.standard_normal(E) * 1.5).astype(np.float32)
+    s = np.array([rows_ref.score(float(v), routing) for v in base])
+    l = np.repeat(base[None], 40, axis=0)
+    l[::2] += (rng.standard_normal((20, E)) * 2.0 ** -22).astype(np.float32)
+    t = dev(l)
+    flat = (0.5 - s).astype(np.float32)
+    for at, far in ((E // 3, -1e9), (E // 3, -3e4), (E // 3, 1e4), (E - 1, 2.0 ** 20), (0, -2.0 ** 120)):
+        b = flat.copy()
+        b[at] = far
+        b[(at + 5) % E] = far                         # the score is lost in the rounding of this sum
+        for score in ("max", "top2"):
+            kw = dict(top_k=8, routing=routing, norm=True, bias=dev(b), groups=G, topk_groups=keep, group_score=score)
+            check_route(t, route_on_gpu(t, **kw), **kw)
+
+
+def route_time(l, **kw):
+    """Microseconds of one call of the routing without a host between the calls: the best of several graphs' replays."""
+    T, E = l.shape
+    bias = kw.get("bias")
+    cfg = B.moe_route_cfg(num_experts=E, top_k=8, routing=B.ROUTING_CODES["sigmoid"], norm_topk_prob=1,
+                          select_on_raw_logits=int(bias is None), has_expert_bias=int(bias is not None),
+                          routed_scaling_factor=1.0, num_groups=8, topk_groups=4, group_score=B.MOE_GROUP_TOP2,
+                          logits_dtype=F32)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx, pairs, perm, off = (torch.empty(n, **i32) for n in (T * 8, T * 8, T * 8, E + 1))
+    w = torch.empty(T * 8, device="cuda")
+    ws = torch.empty(B.moe_route_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    def call():
+        B.moe_route_rows(cfg, T, l, E, bias, idx, w, pairs, off, perm, ws, ws.numel(), torch.cuda.current_stream())
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(20):
+            call()
+    best = float("inf")
+    for _ in range(8):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / 20)
+    return best
+
+
+def test_route_time_does_not_hang_on_one_far_value():
+    """An expert switched off by a large finite bias, or by a logit of the lowest finite number, leaves the other experts'
+    keys as far apart as they were: the rows are still settled in 32 bits."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    l = torch.randn(8191, 256, device="cuda", generator=g)
+    bias = 0.1 * torch.randn(256, device="cuda", generator=g)
+    far = bias.clone()
+    far[100] = -1e9
+    lowest = l.clone()
+    lowest[:, 100] = -F32_MAX
+    times = [route_time(l, bias=bias), route_time(l, bias=far), route_time(l), route_time(lowest)]
+    print("us:", times)
+    assert times[1] < 1.3 * times[0] and times[3] < 1.3 * times[2], times
