@@ -436,19 +436,25 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
     const uint32_t above = __shfl_up_sync(kFull, found, 1);
     const int above_id = __shfl_up_sync(kFull, out.id, 1);
     auto near = [&](float x, float y) { return x - y <= score_err + fmaxf(fabsf(x), fabsf(y)) * kSumErr; };
-    bool close = lane > 0 && found != 0u && near(unordered(above), unordered(found));
+    const bool close = lane > 0 && found != 0u && near(unordered(above), unordered(found));
     if (__any_sync(kFull, close)) {
-      if (close) {   // equal logits with equal biases tie in any arithmetic
-        const size_t row = (size_t)r * (size_t)a.ld;
-        close = load_one(a.logits, row + out.id, a.f32) != load_one(a.logits, row + above_id, a.f32) ||
-                a.bias_p[out.id] != a.bias_p[above_id];
-      }
-      if (__any_sync(kFull, close)) {
-        // the experts found are those of the first k + 1 places if the next is clearly below
-        ordered_ok = false;
-        const uint32_t next = __reduce_max_sync(kFull, key[0]);
-        const uint32_t last = __shfl_sync(kFull, found, a.k);
-        if (next && near(unordered(last), unordered(next))) sure = false;
+      // equal logits with equal biases tie in any arithmetic
+      const size_t row = (size_t)r * (size_t)a.ld;
+      auto tie = [&](int x, int y) {
+        return load_one(a.logits, row + x, a.f32) == load_one(a.logits, row + y, a.f32) && a.bias_p[x] == a.bias_p[y];
+      };
+      if (__any_sync(kFull, close && !tie(out.id, above_id))) ordered_ok = false;
+      // The k best are among the k + 1 found if the last of those is apart from the one before or from all others, or if
+      // the order stands and the others near it tie with it. (Its own tie with the one before says nothing of the
+      // others: they may share its key in 32 bits alone.)
+      if (__shfl_sync(kFull, (int)close, a.k)) {
+        const float last = unordered(__shfl_sync(kFull, found, a.k));
+        const int last_id = __shfl_sync(kFull, out.id, a.k);
+        bool rival = false;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          if (key[j] != 0u && near(last, unordered(key[j]))) rival = rival || !ordered_ok || !tie(id[j], last_id);
+        if (__any_sync(kFull, rival)) sure = false;
       }
     }
   }

@@ -252,3 +252,27 @@ def test_route_time_does_not_hang_on_one_far_value():
     times = [route_time(l, bias=bias), route_time(l, bias=far), route_time(l), route_time(lowest)]
     print("us:", times)
     assert times[1] < 1.3 * times[0] and times[3] < 1.3 * times[2], times
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,G,keep", [(16, 1, 1), (31, 1, 1), (256, 1, 1), (256, 8, 8), (256, 8, 4), (510, 17, 9), (512, 1, 1)])
+def test_route_saturated_scores_rank_beyond_float32(E, G, keep, dtype):
+    """sigmoid(30) and sigmoid(31) are both 1 in 32 bits. Many equal logits come before the one that 64 bits rank first."""
+    rng = np.random.default_rng(E)
+    e = np.arange(E)
+    l = np.full((24, E), 30.0)
+    l[0, E - 1] = 31
+    l[1, E // 2:] = 35
+    l[2] = rng.integers(25, 37, E)
+    l[3] = np.where(e < 2, 30, rng.integers(28, 34, E))
+    l[4] = np.where(e == E - 2, 36, -30)
+    l[5] = e % 3 + 30
+    l[7] = np.where(e % 5 == 4, 33, 30)
+    for r in range(8, 24):
+        l[r] = np.where(rng.random(E) < 0.8, 30, rng.integers(29, 32, E))
+    t = dev(l, dtype)
+    step = np.where(e % 7 == 6, 0.5, 0.25).astype(np.float32)
+    for b in (np.zeros(E, np.float32), np.full(E, 0.25, np.float32), step, -step, 1e6 * step):
+        for k in (1, 3, 8, 15):
+            kw = dict(top_k=k, routing="sigmoid", norm=True, bias=dev(b), groups=G, topk_groups=keep, group_score="top2")
+            check_route(t, route_on_gpu(t, **kw), **kw)
