@@ -174,14 +174,12 @@ lib = _load()
 
 def _ptr(a) -> Optional[int]:
     """Device or host address of ``a``: None, an int, a torch tensor or a numpy array."""
-    if a is None:
-        return None
+    if a is None or isinstance(a, int):
+        return a
     try:
         return a.data_ptr()
     except AttributeError:
         pass
-    if isinstance(a, int):
-        return a
     if isinstance(a, np.ndarray):
         if not a.flags["C_CONTIGUOUS"]:
             raise ValueError("host arrays must be C-contiguous")
