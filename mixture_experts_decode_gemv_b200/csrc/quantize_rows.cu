@@ -218,11 +218,13 @@ cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x
 template <bool F32, int TPR>
 cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
                            float* scales, cudaStream_t st) {
-  const int ng = (groups + TPR - 1) / TPR;
-  if (ng <= 2) return launch_vectors<F32, TPR, 2>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  const int ng = (groups + TPR - 1) / TPR;   // by the caller's rule up to 4 for 32 threads, from 3 on for 512
+  if constexpr (TPR < 512) {
+    if (ng <= 2) return launch_vectors<F32, TPR, 2>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  }
   if (ng <= 3) return launch_vectors<F32, TPR, 3>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
-  if (ng <= 5) return launch_vectors<F32, TPR, 5>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
-  return launch_vectors<F32, TPR, kQGroups>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  if (TPR == 32 || ng <= 5) return launch_vectors<F32, TPR, 5>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
+  if constexpr (TPR > 32) return launch_vectors<F32, TPR, kQGroups>(rows, groups, x, ld_x, codes, ld_codes, scales, st);
 }
 
 // A warp to a row up to 1024 elements, where more threads would idle (65536 rows of 768: 31.7 us against 69

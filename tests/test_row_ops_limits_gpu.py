@@ -6,7 +6,8 @@ import torch
 
 from mixture_experts_decode_gemv_b200 import binding as B
 from oracle import rows_ref
-from test_row_ops_gpu import BF16, DT, F32, Product, check_route, dev, int8_matrix, route_on_gpu, status, workspace
+from test_row_ops_gpu import (BF16, DT, F32, Product, check_quantise, check_route, dev, int8_matrix, quantise_on_gpu,
+                              route_on_gpu, status, workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -276,3 +277,13 @@ def test_route_saturated_scores_rank_beyond_float32(E, G, keep, dtype):
         for k in (1, 3, 8, 15):
             kw = dict(top_k=k, routing="sigmoid", norm=True, bias=dev(b), groups=G, topk_groups=keep, group_score="top2")
             check_route(t, route_on_gpu(t, **kw), **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k", [8 * g for g in (1, 32, 33, 64, 65, 96, 97, 127, 128, 129, 256, 257, 384, 385, 640, 641, 1024, 1025,
+                                              1536, 1537, 2560, 2561, 4096, 4097)])
+def test_quantise_around_every_change_of_the_launch(k, dtype):
+    rng = np.random.default_rng(k)
+    x = dev(rng.standard_normal((5, k)), dtype)
+    x[3, -1] = 40.0
+    check_quantise(x, quantise_on_gpu(x))
