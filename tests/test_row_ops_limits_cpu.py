@@ -39,3 +39,11 @@ def test_addresses_as_plain_integers_are_taken_at_once():
         B._ptr("x")
     with pytest.raises(ValueError):
         B._ptr(np.empty((4, 4))[:, ::2])
+
+
+def test_route_workspace_never_shrinks_where_the_launch_changes():
+    for E in (1, 3, 130, 512):
+        c = B.moe_route_cfg(num_experts=E, top_k=1, routing=0, norm_topk_prob=1, select_on_raw_logits=0, has_expert_bias=0,
+                            routed_scaling_factor=1.0, num_groups=1, topk_groups=1, group_score=0, logits_dtype=B.MOE_FMT_F32)
+        sizes = [B.moe_route_workspace_bytes(c, r) for r in (0, 1, 15, 16, 17, 24, 25, 1183, 1184, 1185, 1193, 2**31 - 1)]
+        assert sizes == sorted(sizes) and all(s % 256 == 0 for s in sizes)

@@ -6,7 +6,7 @@ import torch
 
 from mixture_experts_decode_gemv_b200 import binding as B
 from oracle import rows_ref
-from test_row_ops_gpu import (BF16, DT, F32, Product, check_quantise, check_route, dev, int8_matrix, quantise_on_gpu,
+from test_row_ops_gpu import (BF16, DT, F32, Layer, Product, check_quantise, check_route, dev, int8_matrix, quantise_on_gpu,
                               route_on_gpu, status, workspace)
 
 pytestmark = pytest.mark.gpu
@@ -287,3 +287,66 @@ def test_quantise_around_every_change_of_the_launch(k, dtype):
     x = dev(rng.standard_normal((5, k)), dtype)
     x[3, -1] = 40.0
     check_quantise(x, quantise_on_gpu(x))
+
+
+@pytest.mark.parametrize("rows", [16, 17, 24, 25, 1183, 1184, 1185, 1193])
+@pytest.mark.parametrize("E,G,keep", [(64, 4, 3), (512, 1, 1)])
+def test_route_row_counts_where_the_launch_changes(rows, E, G, keep):
+    """One launch up to 16 rows; blocks of eight rows up to 148 of them (1184 rows), longer blocks beyond."""
+    rng = np.random.default_rng(rows)
+    l = rng.standard_normal((rows, E))
+    l[rows // 2] = -np.inf
+    l[-1, 1:] = -np.inf
+    t = dev(l, torch.float32)
+    kw = dict(top_k=6, routing="sigmoid", norm=True, groups=G, topk_groups=keep)
+    check_route(t, route_on_gpu(t, **kw), **kw)
+
+
+def test_layer_forked_and_joined_in_a_graph():
+    """Two layers on streams of their own between the same ends, captured and replayed: a call waits for all that its
+    stream waits for, whatever kind of work that was."""
+    a, b = Layer(130, 256, 128, 16, 4, seed=1), Layer(60, 256, 128, 16, 4, seed=2)
+    both = torch.empty(190, 256, dtype=torch.bfloat16, device="cuda")
+    gate = torch.ones(130, device="cuda")
+    perm = torch.arange(130, dtype=torch.int32, device="cuda")
+    last = torch.empty(130, 256, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        a.forward(main)
+        with torch.cuda.stream(side):
+            b.forward(side)
+            both[130:].copy_(b.out)
+        both[:130].copy_(a.out)
+        main.wait_stream(side)
+        # reads what both streams wrote
+        B.moe_combine_rows(130, 256, 1, BF16, both[:130], 256, 130, perm, None, both[60:], 256, gate, BF16, last, 256, main)
+        a.x.copy_(last)                               # ... and the next pass reads this
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            run()
+    want = None
+    for replay in (False, True, True):
+        a.set_inputs(5)
+        b.set_inputs(6)
+        torch.cuda.synchronize()
+        if replay:
+            graph.replay()
+        else:
+            for _ in range(3):
+                run()
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (a.out, b.out, both, last)]
+        want = want or got
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert bool(want[3].any()) and status(a.mws) == B.MOE_OK and status(b.mws) == B.MOE_OK
