@@ -314,6 +314,27 @@ enum Verdict { kSure, kOrderOpen, kOpen };
 // every sum by half a unit of its own: a large bias opens nothing but what it enters. What lies below the lower of two
 // keys that are apart is apart from the higher one too: a key and its error grow together.
 constexpr float kSumErr = 0x1.8p-23f;   // of the sums in two keys, or in a group's score and its border, relative to their magnitudes
+
+// Whether 32 bits leave open that a key of x ranks before one of y.
+__device__ __forceinline__ bool near(float x, float y, float score_err) {
+  return x - y <= score_err + fmaxf(fabsf(x), fabsf(y)) * kSumErr;
+}
+__device__ __forceinline__ bool tie(const RouteArgs& a, size_t row, int x, int y) {
+  return load_one(a.logits, row + x, a.f32) == load_one(a.logits, row + y, a.f32) && a.bias_p[x] == a.bias_p[y];
+}
+// Whether an expert of this lane is near `last`, the key of expert `id`, and does not tie with it.
+__device__ __noinline__ bool rival(const RouteArgs& a, const Place& at, size_t row, int id, float last,
+                                   float score_err) {
+  bool found = false;
+  for (int j = 0; j < a.per && at.real(a, j); ++j) {
+    const int e = at.base + j;
+    const float l = fminf(load_one(a.logits, row + e, a.f32), FLT_MAX), b = a.bias_p[e];
+    if (l > -INFINITY && b > -INFINITY && near(last, score_of(a.routing, l) + b, score_err))
+      found = found || !tie(a, row, e, id);
+  }
+  return found;
+}
+
 template <int NJ>
 __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at, long long r, const float (&lg)[NJ],
                                           const float (&bs)[NJ], Slots& out) {
@@ -435,26 +456,20 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
     // gaps between neighbours in the order found
     const uint32_t above = __shfl_up_sync(kFull, found, 1);
     const int above_id = __shfl_up_sync(kFull, out.id, 1);
-    auto near = [&](float x, float y) { return x - y <= score_err + fmaxf(fabsf(x), fabsf(y)) * kSumErr; };
-    const bool close = lane > 0 && found != 0u && near(unordered(above), unordered(found));
+    const bool close = lane > 0 && found != 0u && near(unordered(above), unordered(found), score_err);
     if (__any_sync(kFull, close)) {
       // equal logits with equal biases tie in any arithmetic
       const size_t row = (size_t)r * (size_t)a.ld;
-      auto tie = [&](int x, int y) {
-        return load_one(a.logits, row + x, a.f32) == load_one(a.logits, row + y, a.f32) && a.bias_p[x] == a.bias_p[y];
-      };
-      if (__any_sync(kFull, close && !tie(out.id, above_id))) ordered_ok = false;
+      if (__any_sync(kFull, close && !tie(a, row, out.id, above_id))) ordered_ok = false;
       // The k best are among the k + 1 found if the last of those is apart from the one before or from all others, or if
       // the order stands and the others near it tie with it. (Its own tie with the one before says nothing of the
       // others: they may share its key in 32 bits alone.)
       if (__shfl_sync(kFull, (int)close, a.k)) {
         const float last = unordered(__shfl_sync(kFull, found, a.k));
         const int last_id = __shfl_sync(kFull, out.id, a.k);
-        bool rival = false;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          if (key[j] != 0u && near(last, unordered(key[j]))) rival = rival || !ordered_ok || !tie(id[j], last_id);
-        if (__any_sync(kFull, rival)) sure = false;
+        if (__any_sync(kFull, key[0] != 0u && near(last, unordered(key[0]), score_err)) &&
+            (!ordered_ok || __any_sync(kFull, kept && rival(a, at, row, last_id, last, score_err))))
+          sure = false;
       }
     }
   }
