@@ -324,7 +324,7 @@ int moe_route_workspace_bytes(const moe_route_cfg* cfg, int64_t rows, size_t* ou
  *  weights  [rows, k] s, divided by the sum of the row's k scores when norm_topk_prob, times
  *           routed_scaling_factor
  * Keys and group scores are compared as in 64-bit arithmetic: 32-bit ones decide only where
- * their rounding cannot change the outcome.
+ * their rounding cannot change the outcome. Weights are computed in float32. 0 and -0 are equal.
  * An expert whose logit or key is -infinity or NaN is masked: it is never selected and has no
  * part in softmax; +infinity counts as the largest finite logit. A slot that finds no expert gets
  * idx -1 and weight 0 (a fully masked row: all its slots). Under norm_topk_prob the weights of
@@ -381,6 +381,9 @@ int moe_matmul_workspace_bytes(const moe_matmul_cfg* cfg, int64_t rows, size_t* 
  *  out            [rows, ld_out] in cfg->out_dtype
  *  workspace      moe_matmul_workspace_bytes(cfg, rows) bytes, 256-byte aligned, initialised once
  *                 by moe_workspace_init; moe_get_device_status reads its status
+ * The factors and the activation are float32: a plain output is within 4 roundings (2^-24 each) of its value before the
+ * rounding to out_dtype; SwiGLU's exponential adds 2 + 1.2 |g| units of 2^-23 for a gate g. A product of the
+ * factors beyond float32 becomes infinite (and the activation of a gate of -infinity NaN).
  * Calls that share a workspace must be ordered. A NaN scale gives NaN outputs. */
 int moe_matmul_int8(const moe_matmul_cfg* cfg, int64_t x_rows, const int8_t* x, int64_t ld_x,
                     const float* x_scales, int64_t rows, const int32_t* expert_offsets,

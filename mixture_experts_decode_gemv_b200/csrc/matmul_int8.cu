@@ -278,8 +278,8 @@ __device__ __forceinline__ void write_tile(const MatmulArgs& a, T* out, uint32_t
 // Two blocks share a tile of 256 channels (128 with gate and up) x up to 256 rows: each loads half of
 // both operands and holds the accumulators of its channels (int32, 256 columns of tensor memory, two
 // buffers, so that one tile is written out while the next is multiplied). Per step of 128 bytes of k a block loads 32 KB
-// for 512 cycles of MMA. 4099 rows, 2 x 8192 channels, k = 5120: 250 us, 2.75 POP/s, at the power cap (1345 MHz) with the
-// tensor pipe busy 96 % of the cycles; over 128 experts, where tiles are short, it is busy 45 to 55 %.
+// for 512 cycles of MMA. 4099 rows, 2 x 8192 channels, k = 5120: 253 us, 2.72 POP/s, at the power cap (1320 MHz) with the
+// tensor pipe busy 96 % of the cycles; over 128 experts, where tiles are short, it is busy 44 to 55 %.
 template <int ACT>
 __global__ void __launch_bounds__(kPairThreads, 1)
 matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ CUtensorMap map_x,
@@ -556,7 +556,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__
 // to clear. (Two blocks of 16 or 32 rows and five or four stages on a multiprocessor took 46.5 and 49.0 us
 // against 45.9 for one of 64 rows and seven, 16 rows x 8 of 128 experts, 2 x 768 channels, k = 2048; 61.4
 // and 64.3 against 61.2 with 64 rows.)
-// One row, 5120 channels, k = 8192: 11.2 us (42 MB; about 5 us are launch, first loads and exchange); 16 rows x 8 of 128
+// One row, 5120 channels, k = 8192: 11.3 us (42 MB; about 5 us are launch, first loads and exchange); 16 rows x 8 of 128
 // experts, 2 x 768 channels, k = 2048: 41.5 us (256 MB, 6.1 TB/s).
 constexpr int kFewThreads = 256;    // warp 0 weights, 1 MMAs, 2 and 3 rows of x, 4 to 7 write out
 constexpr int kFewMaxCluster = 8;
@@ -732,7 +732,7 @@ matmul_few_kernel(const __grid_constant__ MatmulArgs a, const __grid_constant__ 
     // column c of the sums goes to block c % split, which adds it up and writes its row
     const int quarter = warp & 3, lane_ch = quarter * 32 + lane;
     const bool up = ACT && ((lane & 16) != 0) != a.up_first;
-    // The exchange. Up to kFewHalf rows a tile, the sums of odd and even tiles lie apart, and nothing else keeps a
+    // The exchange. With up to kFewHalf rows in every tile, the sums of odd and even tiles lie apart, and nothing else keeps a
     // tile's stores behind the reads of the tile that had its place: a block has seen the sums of the tile between
     // them arrive from every warp of the cluster, each of which had read the older one. More rows take the whole of
     // `red`, and say on red_free that they have read it, which costs 0.4 us a tile (one row, 20480 channels, k = 8192:

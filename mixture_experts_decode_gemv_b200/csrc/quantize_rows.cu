@@ -7,7 +7,7 @@
 // x and q0 * scale are multiples of half an ulp of the scale, and where the choice is open (r near
 // half a scale) r needs at most 24 bits. Comparing r with scale / 2 corrects q0.
 //
-// Bound by memory: each element is read once and one byte is written (8192 x 5120 bf16: 19.8 us, 6.35 TB/s). A row stays in the registers of
+// Bound by memory: each element is read once and one byte is written (8192 x 5120 bf16: 20.7 us, 6.1 TB/s). A row stays in the registers of
 // the threads that read it (32, 128 or 512 of them, eight elements to a load) between the pass for its
 // maximum and the pass that rounds. The ordinary element costs five instructions: the quotient rounded
 // by adding 1.5 * 2^23 in the fma that forms it, the remainder, and its largest magnitude so far; only
@@ -228,8 +228,8 @@ cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x
 }
 
 // A warp to a row up to 1024 elements, where more threads would idle (65536 rows of 768: 31.7 us against 69
-// with 128 threads to a row); 128 threads up to 8192 (64 rows of 2048: 1.8 us against 2.8 with a warp; 8192
-// of 2048: 12.0 against 13.8); 512 beyond.
+// with 128 threads to a row); 128 threads up to 8192 (64 rows of 2048: 1.4 us against 2.8 with a warp; 8192
+// of 2048: 12.0 against 13.8, 10.2 now); 512 beyond.
 template <bool F32>
 cudaError_t launch_vectors(int64_t rows, int groups, const void* x, int64_t ld_x, int8_t* codes, int64_t ld_codes,
                            float* scales, cudaStream_t st) {

@@ -11,9 +11,9 @@
 // magnitudes that it is made of; when two that decide something lie closer than such errors may add up to
 // (2^-20 of the one, 3 * 2^-24 of the other), the row is settled in float64 (a few rows in a thousand).
 //
-// Bound by issue slots (69 % active, 13.8 M warp instructions): 8191 rows of 256 experts, best 4 of 8 groups, top 8
-// with a bias, take 24 us, 6 of them the grouping; the logits alone would take 1.4 from HBM. A row that is settled in
-// float64 costs its warp about 3 us.
+// Bound by instructions (12.0 M of the warps, 66 % of the issue slots; 3 % of them are spills, as 1024 threads to a block
+// leave 64 registers to a thread): 8191 rows of 256 experts, best 4 of 8 groups, top 8 with a bias, take 23 us, 6 of them the
+// grouping; the logits alone would take 1.4 from HBM. A row that is settled in float64 costs its warp about 3 us.
 //
 // Grouping is a stable counting sort: blocks of rows count their pairs per expert into a table,
 // and a second launch turns the table into positions (rows that fit one block do both in one
@@ -313,7 +313,7 @@ enum Verdict { kSure, kOrderOpen, kOpen };
 // largest (fast exponential and reciprocal; 16 for softmax, whose scores carry the denominator's rounding too), and
 // every sum by half a unit of its own: a large bias opens nothing but what it enters. What lies below the lower of two
 // keys that are apart is apart from the higher one too: a key and its error grow together.
-constexpr float kSumErr = 0x1.8p-23f;   // of the sums in two keys, or in a group's score and its border, relative to their magnitudes
+constexpr float kSumErr = 0x1.8p-23f;   // of the sums in two keys or in a group's score, relative to their magnitudes
 
 // Whether 32 bits leave open that a key of x ranks before one of y.
 __device__ __forceinline__ bool near(float x, float y, float score_err) {
