@@ -377,7 +377,8 @@ __device__ __forceinline__ Verdict route_row(const RouteArgs& a, const Place& at
       mag = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
     }
   }
-  const float score_err = mag * (soft ? 0x1p-18f : 0x1p-20f);   // of two scores
+  // of two scores; below the normal numbers errors are no longer relative, and float64 decides
+  const float score_err = fmaf(mag, soft ? 0x1p-18f : 0x1p-20f, FLT_MIN);
   float kf[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) kf[j] = a.bias && lg[j] > -INFINITY ? sc[j] + bs[j] : lg[j];

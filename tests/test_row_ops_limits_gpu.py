@@ -350,3 +350,14 @@ def test_layer_forked_and_joined_in_a_graph():
         want = want or got
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert bool(want[3].any()) and status(a.mws) == B.MOE_OK and status(b.mws) == B.MOE_OK
+
+
+@pytest.mark.parametrize("lo,hi", [(-206, -176), (-190, -188), (-200, -199.5), (-172, -171.9)])
+def test_route_scores_below_the_normal_numbers(lo, hi):
+    """sqrt(softplus(l)) = e^(l/2) has a few bits left in 32 bits, or none."""
+    t = dev(np.random.default_rng(3).uniform(lo, hi, (200, 64)), torch.float32)
+    zero = torch.zeros(64, device="cuda")
+    for kw in (dict(bias=zero), dict(bias=zero, groups=8, topk_groups=3, group_score="top2"),
+               dict(groups=8, topk_groups=3, group_score="top2")):
+        kw = dict(kw, top_k=8, routing="sqrtsoftplus", norm=True)
+        check_route(t, route_on_gpu(t, **kw), **kw)
